@@ -300,7 +300,7 @@ def _own(s):
     else:
         s["refs"].copy_(s["refs0"])
         s["tables"].copy_(s["tables0"])
-        xq.xq_cache_compact(s["kv"], s["refs"], s["tables"], s["lens"], s["status"], workspace=s["ws"])
+        xq.xq_cache_compact(s["kv"], s["refs"], s["tables"], s["status"], workspace=s["ws"])
     return s["k"], s["v"], s["refs"], s["tables"], s["lens"], s["status"]
 
 
