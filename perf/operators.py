@@ -422,7 +422,7 @@ def _plain_pages(s):
         refs.index_add_(0, new, part.int())
         tables[kids] = torch.where(shared, rows, torch.where(tail, new[:, None].int(), -1))
         lens[kids] = n
-        _move(s, last, torch.where(part, new, last))
+        _move(s, last[part], new[part])                                 # a full last page is shared, not copied
         s["status"].zero_()
     else:
         refs.copy_(s["refs0"])
