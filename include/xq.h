@@ -12,9 +12,11 @@
  *    ("cajeta.xpu — one kernel, any device", section 2.2: buffers are the
  *    caller's allocations). The library allocates no memory and keeps no
  *    per-call state; it never synchronizes a stream or the device.
- *  - Three entry points need device scratch beyond their inputs and outputs
+ *  - Six entry points need device scratch beyond their inputs and outputs
  *    (xq_gemm_q4k_small_m's split-K partials and arrival counters,
- *    xq_gemv_q4k_q8k's arrival counters, xq_gemm_q4k_id's expert map). The
+ *    xq_gemv_q4k_q8k's arrival counters, xq_gemm_q4k_id's expert map,
+ *    xq_attn_decode's split partials and arrival counters, the lists of
+ *    xq_cache_fork and xq_cache_compact). The
  *    caller passes it as `workspace` (device memory, 256-byte aligned) and
  *    `workspace_bytes`; the matching *_workspace_bytes query gives the exact
  *    bytes a call needs (0: none, and then workspace may be NULL). The caller
@@ -328,6 +330,204 @@ xq_status xq_gemv_iq4nl_id(float *y, const void *slab, const void *xq, const int
 xq_status xq_repack_iq4nl(void *resident, const void *file_blocks, int64_t n_blocks,
                           int64_t block_base, int64_t bpr, void *stream);
 int64_t xq_repack_dword_prefix_launches(void);
+
+/* ---- The paged key-value cache: attention, rotary positions, pages ----
+ *
+ * The calls below are what a decode step needs beside its mat-vecs. Their
+ * conventions are those above, and in addition:
+ *  - Strides are in elements of the tensor they belong to; the head dimension
+ *    (dim) is always contiguous.
+ *  - Lengths, tables, positions, slots and reference counts are device data
+ *    that the host never reads. What the kernels find in them they check
+ *    against the sizes of the call: a length is clamped to what the table
+ *    (and max_len) can hold, a page number outside 0..pages-1 hides that
+ *    page's tokens, a slot outside the cache drops its token. No value in
+ *    them makes a kernel read or write outside its buffers.
+ */
+
+/* Element types. */
+enum { XQ_F32 = 0, XQ_BF16 = 1, XQ_F16 = 2, XQ_E4M3 = 3 };
+
+/*
+ * A paged cache, a host struct that describes device memory. Token j of a
+ * sequence lies in page table[j / page] at slot j % page. Element
+ * (layer l, page p, head h, slot s, d) of k is at
+ *   k + l * k_stride[0] + p * k_stride[1] + h * k_stride[2] + s * k_stride[3] + d
+ * (v the same with v_stride), so pages stored head by head or token by token
+ * are both just strides.
+ *  dtype  XQ_BF16, XQ_F16 or XQ_E4M3 (8 bits, 4 exponent, 3 mantissa, largest
+ *         448, no infinity). What a stored k stands for is k * k_scale, a
+ *         stored v is v * v_scale, in every type; both finite and above 0.
+ *  1 <= layers, pages, page, kv_heads; pages * page <= 2^31 - 1 (a slot is an
+ *  int32's worth; byte offsets are 64-bit). dim a multiple of 16, 16..256.
+ *  k and v 16-byte aligned; strides >= 0 and multiples of 16 bytes.
+ * Attention and the append work on one layer (layers = 1: a layer of a larger
+ * cache is the struct with k and v advanced).
+ */
+typedef struct {
+    void *k, *v;
+    int64_t layers, pages, kv_heads, page, dim;
+    int64_t k_stride[4], v_stride[4];
+    int32_t dtype;
+    float k_scale, v_scale;
+} xq_kv;
+
+/*
+ * Attention of one new token per sequence over the paged cache. Sequence b
+ * has lens[b] tokens in the cache, the new one the last of them. With n =
+ * lens[b] and g = h / (heads / kv_heads), token j is visible when j < n and
+ * (window = 0, or j >= n - window, or j < sinks), and
+ *   out[b][h] = sum_j p_j * v_scale * v_j[g],
+ *   p = softmax over the visible j of scale * k_scale * (q[b][h] . k_j[g]).
+ * A sequence with no visible token gives zeros; a visible infinity or NaN in v
+ * reaches the dims that it is in (in k, a NaN of every dim). Sums, maxima and products are
+ * held in f32; q and the weights p enter the matrix instructions as two or
+ * three 16-bit pieces where one would round them below the output's type.
+ *
+ *  out, q   device [seqs][heads][dim] of type io (XQ_F32, XQ_BF16, XQ_F16),
+ *           strides per sequence (row) and head, both a multiple of 16 bytes;
+ *           bases 16-byte aligned.
+ *  tables   device int32, row b at tables + b * table_stride, table_width
+ *           pages per row; lens device int32[seqs].
+ *  heads a multiple of kv_heads, heads / kv_heads <= 256, seqs * kv_heads <= 2^20.
+ *  window in 0..2^30 (0: none), sinks in 0..2^30 (read only with a window).
+ *  max_len in 1..2^30: no length is above it (longer ones are clamped); the split of
+ *  the work is planned for it, the result of a given plan is the same from
+ *  call to call, bit for bit.
+ *  workspace  the splits' partial results and arrival counters:
+ *      xq_attn_decode_workspace_bytes(...) bytes with the same arguments
+ *      (0 when the plan does not split), zeroed before first use.
+ * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
+ */
+xq_status xq_attn_decode(void *out, const void *q, int32_t io, int64_t seqs, int64_t heads,
+                         int64_t out_row, int64_t out_head, int64_t q_row, int64_t q_head,
+                         const xq_kv *kv, const int32_t *tables, int64_t table_width,
+                         int64_t table_stride, const int32_t *lens, float scale, int64_t window,
+                         int64_t sinks, int64_t max_len, void *workspace, size_t workspace_bytes,
+                         void *stream);
+size_t xq_attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv *kv,
+                                      int64_t max_len, int64_t window, int64_t sinks);
+
+/*
+ * Attention of a chunk of new tokens per sequence over the paged cache, which
+ * already holds them (xq_rope_append). Sequence b's rows of q are
+ * starts[b] .. starts[b+1]-1; with c of them and n = lens[b], row i has
+ * position p = n - c + i and sees token j when j <= p and (window = 0, or
+ * j > p - window, or j < sinks). The sum is xq_attn_decode's. A row that sees
+ * nothing (a position below 0, pages that are missing) gives zeros. A token
+ * that a row does not see has no influence on it, whatever its bytes are.
+ * The weights p are rounded to the cache's type (io for an 8-bit cache)
+ * before their product with v; sums and maxima are f32.
+ *
+ *  out, q   device [rows][heads][dim] of type io, XQ_BF16 or XQ_F16; the
+ *           cache's type is io or XQ_E4M3. Strides and alignment as in
+ *           xq_attn_decode. Rows of out that no sequence names stay as they are.
+ *  starts   device int32[seqs + 1], ascending from >= 0 to <= rows; a
+ *           sequence's part outside 0..rows or beyond max_chunk is left out.
+ *  max_chunk in 1..rows: the longest chunk; rows * heads <= 2^31 - 1, seqs <= 2^16.
+ * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
+ */
+xq_status xq_attn_prefill(void *out, const void *q, int32_t io, int64_t rows, int64_t seqs,
+                          int64_t heads, int64_t out_row, int64_t out_head, int64_t q_row,
+                          int64_t q_head, const xq_kv *kv, const int32_t *tables,
+                          int64_t table_width, int64_t table_stride, const int32_t *lens,
+                          const int32_t *starts, int64_t max_chunk, float scale, int64_t window,
+                          int64_t sinks, void *stream);
+
+/*
+ * Rotary positions with one to four axes (a text has one; an image or a video
+ * has time, height and width). The first `rot` elements of each head form
+ * rot/2 pairs: (i, i + rot/2), or (2i, 2i + 1) when `adjacent` is 1. Pairs are
+ * dealt to the axes in order, sections[0] to axis 0 and so on (their sum is
+ * rot/2). Pair i of token t turns by pos[axis][t] * freq[i]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos);
+ * elements from rot on are copied. inverse = 1 turns the other way, which is
+ * the gradient's direction (the rotation's transpose). The angle is formed
+ * and reduced in f64, its sine and cosine are f32.
+ */
+typedef struct {
+    const double *freq;   /* device f64[rot/2], 8-byte aligned */
+    int64_t rot, axes, adjacent;
+    int64_t sections[4];  /* >= 0; those from `axes` on are ignored */
+} xq_rope_freqs;
+
+/*
+ *  out  device [tokens][heads][dim] of type out_type, x of type x_type (each
+ *       XQ_F32, XQ_BF16 or XQ_F16), aligned to their elements. out may be x
+ *       where types and strides are the same.
+ *  pos  device int32, axis a's positions at pos + a * pos_stride.
+ *  tokens, heads >= 1, tokens * heads <= 2^31 - 1; dim a multiple of 8, 8..1024;
+ *  rot a multiple of 8, 8..dim.
+ * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
+ */
+xq_status xq_rope(void *out, int32_t out_type, int64_t out_row, int64_t out_head, const void *x,
+                  int32_t x_type, int64_t x_row, int64_t x_head, int64_t tokens, int64_t heads,
+                  int64_t dim, const int32_t *pos, int64_t pos_stride, const xq_rope_freqs *rope,
+                  int32_t inverse, void *stream);
+
+/*
+ * The same rotation of q and k, fused with the append of k and v to the
+ * cache: q_out = rope(q); token t's rope(k) / k_scale and v / v_scale go to
+ * slot slots[t] (page slots[t] / page, place slots[t] % page), rounded once to
+ * the cache's type (XQ_E4M3: clamped to +-448). A slot outside
+ * 0..pages*page-1 writes nothing to the cache. No two tokens may have the same
+ * slot.
+ *  q, k, v  device [tokens][heads or kv_heads][dim] of one type x_type (XQ_F32,
+ *           XQ_BF16, XQ_F16), each with its own strides (slices of one
+ *           product's output are fine). slots device int64[tokens].
+ * Sizes and errors as xq_rope, dim as the cache's.
+ */
+xq_status xq_rope_append(void *q_out, int32_t out_type, int64_t out_row, int64_t out_head,
+                         const xq_kv *kv, const void *q, int64_t q_row, int64_t q_head,
+                         const void *k, int64_t k_row, int64_t k_head, const void *v,
+                         int64_t v_row, int64_t v_head, int32_t x_type, int64_t tokens,
+                         int64_t heads, const int32_t *pos, int64_t pos_stride,
+                         const xq_rope_freqs *rope, const int64_t *slots, void *stream);
+
+/*
+ * The pages of a cache, all its layers at once. refs[p] counts the table
+ * entries that name page p; 0 is free. A table row holds a sequence's pages
+ * in order, then -1.
+ *
+ * xq_cache_copy: page src[i] -> page dst[i] for i < n. No page is named twice
+ *   in dst, nor in both lists (unless src[i] = dst[i]); a pair with a page
+ *   outside 0..pages-1 is skipped. n may be 0.
+ * xq_cache_free: for i < n, row rows[i] (skipped outside 0..slots-1) gives its
+ *   pages back: refs[p] -= 1 for each entry, the entries become -1, lens 0. A
+ *   row named twice is freed once. (Where n is 0 the lists may be NULL.)
+ * xq_cache_fork: for i < n, row children[i], which must be empty (lens 0),
+ *   becomes a copy of row parents[i] as it was before the call: full pages are
+ *   shared (refs + 1), a part-filled last page is copied into a fresh one.
+ *   Fresh pages are the free ones in ascending order, taken in the order of
+ *   i, so the result does not depend on timing. A fork is refused when a row
+ *   is out of range, its child is not empty or named before, its parent's row
+ *   is shorter than its length or has a bad page; its child stays empty. When
+ *   the free pages run out the remaining forks that need one are refused too.
+ *   status[0] = refused forks, status[1] = free pages that were lacking.
+ * xq_cache_compact: the live pages (refs > 0) move to 0..live-1: those at or
+ *   above `live`, ascending, into the free ones below it, ascending. Tables and
+ *   refs follow. status[0] = 0, status[1] = live.
+ *
+ *  refs   device int32[pages]; tables device int32 [slots][width] with a
+ *         stride; lens device int32[slots]; status device int32[2].
+ *  1 <= slots <= 2^20; n >= 0, at most 2^20 (copy: 2^31 - 1; fork: slots).
+ *  workspace  (fork, compact) xq_cache_workspace_bytes(pages, slots) bytes,
+ *         rewritten by every call but for the first 96 KiB (other calls' counters).
+ * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
+ */
+xq_status xq_cache_copy(const xq_kv *kv, const int32_t *src, const int32_t *dst, int64_t n,
+                        void *stream);
+xq_status xq_cache_free(const xq_kv *kv, int32_t *refs, int32_t *tables, int64_t slots,
+                        int64_t width, int64_t stride, int32_t *lens, const int32_t *rows,
+                        int64_t n, void *stream);
+xq_status xq_cache_fork(const xq_kv *kv, int32_t *refs, int32_t *tables, int64_t slots,
+                        int64_t width, int64_t stride, int32_t *lens, const int32_t *parents,
+                        const int32_t *children, int64_t n, int32_t *status, void *workspace,
+                        size_t workspace_bytes, void *stream);
+xq_status xq_cache_compact(const xq_kv *kv, int32_t *refs, int32_t *tables, int64_t slots,
+                           int64_t width, int64_t stride, int32_t *status, void *workspace,
+                           size_t workspace_bytes, void *stream);
+size_t xq_cache_workspace_bytes(int64_t pages, int64_t slots);
 
 /*
  * Measurement helper, not part of the method: read `bytes` of device memory

@@ -8,7 +8,7 @@ the layout the C function will read or write, so a wrong-sized buffer is
 refused on the host instead of being read out of bounds. Every step of the
 computation runs in the library's HIP kernels; there is no host path.
 
-Three calls take a caller-owned device workspace (``workspace=``, a device
+Some calls take a caller-owned device workspace (``workspace=``, a device
 tensor of at least the bytes the matching ``*_workspace_bytes`` query gives,
 zeroed before its first use); the binding passes it through and allocates
 nothing.
@@ -36,6 +36,8 @@ EXPORTS = (
     "xq_repack_iq4nl", "xq_repack_dword_prefix_launches", "xq_gemv_q4_0", "xq_gemm_q4k_id",
     "xq_gemv_q4k_q8k", "xq_gemm_q4k_small_m_workspace_bytes", "xq_gemv_q4k_q8k_workspace_bytes",
     "xq_gemm_q4k_id_workspace_bytes", "xq_gemm_q4k_small_m_noalloc",
+    "xq_attn_decode", "xq_attn_decode_workspace_bytes", "xq_attn_prefill", "xq_rope", "xq_rope_append",
+    "xq_cache_copy", "xq_cache_free", "xq_cache_fork", "xq_cache_compact", "xq_cache_workspace_bytes",
 )
 XQ_NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024
 
@@ -87,6 +89,22 @@ def lib() -> ctypes.CDLL:
                 getattr(L, f).restype = ctypes.c_size_t
             L.xq_bench_sink_words.argtypes = [I]
             L.xq_bench_sink_words.restype = I
+            F = ctypes.c_float
+            L.xq_attn_decode.argtypes = [P, P, S, I, I, I, I, I, I, P, P, I, I, P, F, I, I, I, P, Z, P]
+            L.xq_attn_prefill.argtypes = [P, P, S, I, I, I, I, I, I, I, P, P, I, I, P, P, I, F, I, I, P]
+            L.xq_rope.argtypes = [P, S, I, I, P, S, I, I, I, I, I, P, I, P, S, P]
+            L.xq_rope_append.argtypes = [P, S, I, I, P, P, I, I, P, I, I, P, I, I, S, I, I, P, I, P, P, P]
+            L.xq_cache_copy.argtypes = [P, P, P, I, P]
+            L.xq_cache_free.argtypes = [P, P, P, I, I, I, P, P, I, P]
+            L.xq_cache_fork.argtypes = [P, P, P, I, I, I, P, P, P, I, P, P, Z, P]
+            L.xq_cache_compact.argtypes = [P, P, P, I, I, I, P, P, Z, P]
+            for f in ("xq_attn_decode", "xq_attn_prefill", "xq_rope", "xq_rope_append", "xq_cache_copy",
+                      "xq_cache_free", "xq_cache_fork", "xq_cache_compact"):
+                getattr(L, f).restype = S
+            L.xq_attn_decode_workspace_bytes.argtypes = [I, I, P, I, I, I]
+            L.xq_cache_workspace_bytes.argtypes = [I, I]
+            for f in ("xq_attn_decode_workspace_bytes", "xq_cache_workspace_bytes"):
+                getattr(L, f).restype = Z
             L.xq_status_name.argtypes = [S]
             L.xq_status_name.restype = ctypes.c_char_p
             L.xq_last_error.argtypes = []
@@ -280,3 +298,9 @@ def xq_bench_stream_read(buf, nbytes: int, sink, stream=None) -> None:
                                       _ptr(sink, 4 * xq_bench_sink_words(nbytes), "sink"),
                                       _stream(stream)),
            "xq_bench_stream_read")
+
+
+from .kv import (  # noqa: E402  (they use the helpers above)
+    XQ_BF16, XQ_E4M3, XQ_F16, XQ_F32, xq_attn_decode, xq_attn_decode_workspace_bytes,
+    xq_attn_prefill, xq_cache_compact, xq_cache_copy, xq_cache_fork, xq_cache_free,
+    xq_cache_workspace_bytes, xq_kv_cache, xq_rope, xq_rope_append, xq_rope_plan)

@@ -38,7 +38,12 @@ SOURCES = [
     "repack_iq4nl.hip",
     "route_experts.hip",
     "stream_read.hip",
+    "attn_decode.hip",
+    "attn_prefill.hip",
+    "rope.hip",
+    "kv_pages.hip",
     "xq_api.cpp",
+    "kv_api.cpp",
 ]
 
 FLAGS = [

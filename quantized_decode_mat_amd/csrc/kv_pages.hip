@@ -1,0 +1,410 @@
+// kv_pages.hip — the pages of a cache: copied, given back, forked, moved
+// together.
+//
+// What bounds them: the bytes of the pages that move, read once and written
+// once; the rest is a few passes over the reference counts and tables. What
+// the host cannot know (which pages are free, how many move) is worked out on
+// the device: one workgroup writes a list of (from, to) pages into the
+// workspace, and a second launch whose size the host bounds moves them. Every
+// allocation takes the lowest free pages in the order of the request, found by
+// a scan, so results do not depend on timing.
+#include <algorithm>
+
+#include "kv_device.h"
+#include "kv_launch.h"
+
+namespace xq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kListThreads = 1024;
+// The first bytes of a workspace are where other calls keep counters that
+// have to stay zero.
+constexpr size_t kCounterRegion = 96 * 1024;
+
+struct PageArgs {
+  uint8_t* base[2];                           // k, v
+  int64_t layer[2], page[2], head[2], tok[2]; // bytes
+  int64_t rows_bytes;                         // dim in bytes
+  int64_t whole;                              // bytes of a page of one layer, when it is one run; else 0
+  int layers, kv_heads, page_tokens, pages;
+  int pieces;                                 // workgroups that share a page of one layer
+};
+
+// One page of one layer of k or v, or a part of it: 16-byte words.
+__device__ __forceinline__ void copy_page(const PageArgs& a, int which, int layer, int piece,
+                                          int64_t from, int64_t to) {
+  const uint8_t* src = a.base[which] + layer * a.layer[which] + from * a.page[which];
+  uint8_t* dst = a.base[which] + layer * a.layer[which] + to * a.page[which];
+  if (a.whole) {
+    const int64_t words = a.whole / 16;
+    const u32x4* s = reinterpret_cast<const u32x4*>(src);
+    u32x4* d = reinterpret_cast<u32x4*>(dst);
+    const int64_t step = static_cast<int64_t>(kThreads) * a.pieces;
+    int64_t i = static_cast<int64_t>(piece) * kThreads + threadIdx.x;
+    for (; i + 3 * step < words; i += 4 * step) {
+      const u32x4 w0 = s[i], w1 = s[i + step], w2 = s[i + 2 * step], w3 = s[i + 3 * step];
+      d[i] = w0;
+      d[i + step] = w1;
+      d[i + 2 * step] = w2;
+      d[i + 3 * step] = w3;
+    }
+    for (; i < words; i += step) d[i] = s[i];
+  } else {
+    const int row_words = static_cast<int>(a.rows_bytes / 16);
+    const int64_t words = static_cast<int64_t>(a.kv_heads) * a.page_tokens * row_words;
+    for (int64_t i = static_cast<int64_t>(piece) * kThreads + threadIdx.x; i < words;
+         i += static_cast<int64_t>(kThreads) * a.pieces) {
+      const int64_t row = i / row_words;
+      const int64_t at = (row / a.page_tokens) * a.head[which] + (row % a.page_tokens) * a.tok[which] +
+                         (i - row * row_words) * 16;
+      *reinterpret_cast<u32x4*>(dst + at) = *reinterpret_cast<const u32x4*>(src + at);
+    }
+  }
+}
+
+// Jobs are (pair, layer, k or v, piece), piece fastest; a workgroup walks over
+// them by the grid's size. `count` is on the device where the host does not
+// know it.
+__device__ __forceinline__ void copy_pairs(const PageArgs& a, const int32_t* src, const int32_t* dst,
+                                           int64_t n, int64_t block, int64_t blocks) {
+  const int64_t per = static_cast<int64_t>(a.layers) * 2 * a.pieces;
+  for (int64_t job = block; job < n * per; job += blocks) {
+    const int64_t pair = job / per;
+    const int rest = static_cast<int>(job - pair * per);
+    const int from = src[pair], to = dst[pair];
+    if (static_cast<uint32_t>(from) >= static_cast<uint32_t>(a.pages) ||
+        static_cast<uint32_t>(to) >= static_cast<uint32_t>(a.pages) || from == to)
+      continue;
+    copy_page(a, (rest / a.pieces) % 2, rest / a.pieces / 2, rest % a.pieces, from, to);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void copy_kernel(PageArgs a, const int32_t* src,
+                                                        const int32_t* dst, int64_t n) {
+  copy_pairs(a, src, dst, n, blockIdx.x, gridDim.x);
+}
+
+__global__ __launch_bounds__(kThreads) void free_kernel(int32_t* refs, int pages, int32_t* tables,
+                                                        int slots, int width, int64_t stride,
+                                                        int32_t* lens, const int32_t* rows) {
+  const int row = rows[blockIdx.x];
+  if (row < 0 || row >= slots) return;
+  for (int i = threadIdx.x; i < width; i += kThreads) {
+    // The exchange hands an entry to one of two workgroups with the same row.
+    const int page = atomicExch(tables + row * stride + i, -1);
+    if (page >= 0 && page < pages) atomicSub(refs + page, 1);
+  }
+  if (threadIdx.x == 0) lens[row] = 0;
+}
+
+// Exclusive sum over the workgroup's 1024 threads, and the total.
+__device__ __forceinline__ int group_scan(int v, int* total) {
+  __shared__ int sums[kListThreads / kWave];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int u = __shfl_up(x, d, kWave);
+    if (lane >= d) x += u;
+  }
+  if (lane == kWave - 1) sums[wave] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kListThreads / kWave; ++i) {
+    const int s = sums[i];
+    before += i < wave ? s : 0;
+    all += s;
+  }
+  __syncthreads();
+  *total = all;
+  return before + x - v;
+}
+
+struct TableArgs {
+  int32_t* refs;
+  int32_t* tables;
+  int32_t* lens;
+  const int32_t* parents;
+  const int32_t* children;
+  int32_t* status;
+  int64_t stride;
+  int slots, width, n, pages, page;
+  // Workspace.
+  int32_t* claim;  // [slots]: the first fork that names this child
+  int32_t* src;    // [n or pages]: pages to copy, -1 for none
+  int32_t* dst;
+  int32_t* len;    // [n]: the parent's length before the call; -1: the fork is refused
+  int32_t* map;    // [pages]
+  int32_t* count;
+};
+
+// Forks, first launch: which are sound, and a fresh page for each that needs
+// one.
+__global__ __launch_bounds__(kListThreads) void fork_list_kernel(TableArgs a) {
+  const int tid = threadIdx.x;
+  for (int i = tid; i < a.slots; i += kListThreads) a.claim[i] = a.n;
+  __syncthreads();
+  for (int i = tid; i < a.n; i += kListThreads) {
+    const int c = a.children[i];
+    if (c >= 0 && c < a.slots) atomicMin(a.claim + c, i);
+  }
+  __syncthreads();
+  // A wave checks a fork, its lanes the parent's pages.
+  const int lane = tid % kWave;
+  for (int i = tid / kWave; i < a.n; i += kListThreads / kWave) {
+    const int c = a.children[i], p = a.parents[i];
+    int len = -1;
+    if (c >= 0 && c < a.slots && p >= 0 && p < a.slots &&
+        __hip_atomic_load(a.claim + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == i &&
+        a.lens[c] == 0)
+      len = a.lens[p];
+    const int64_t pages = len < 0 ? 0 : (static_cast<int64_t>(len) + a.page - 1) / a.page;
+    if (pages > a.width) len = -1;
+    int bad = 0;
+    if (len > 0)
+      for (int k = lane; k < pages; k += kWave)
+        bad |= static_cast<uint32_t>(a.tables[p * a.stride + k]) >= static_cast<uint32_t>(a.pages);
+    if (__ballot(bad)) len = -1;
+    if (lane == 0) a.len[i] = len;
+  }
+  __syncthreads();
+  // How many fresh pages, and each fork's number among those that need one.
+  int need = 0, refused = 0;
+  for (int i0 = 0; i0 < a.n; i0 += kListThreads) {
+    const int i = i0 + tid;
+    const int len = i < a.n ? a.len[i] : 0;
+    const int part = len > 0 && len % a.page > 0;
+    refused += len < 0;
+    int total;
+    const int at = need + group_scan(part, &total);
+    if (i < a.n) a.src[i] = part ? at : -1;
+    need += total;
+  }
+  __syncthreads();
+  // The first `need` free pages, ascending, into dst by number.
+  int found = 0;
+  for (int p0 = 0; p0 < a.pages && found < need; p0 += kListThreads) {
+    const int p = p0 + tid;
+    const int is_free = p < a.pages && a.refs[p] == 0;
+    int total;
+    const int at = found + group_scan(is_free, &total);
+    if (is_free && at < need) a.map[at] = p;
+    found += total;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.n; i += kListThreads) {
+    const int at = a.src[i];
+    int from = -1, to = -1;
+    if (at >= 0) {
+      if (at < found) {
+        to = a.map[at];
+        from = a.tables[a.parents[i] * a.stride + a.len[i] / a.page];
+        a.refs[to] = 1;
+      } else {
+        a.len[i] = -1;
+        ++refused;
+      }
+    }
+    a.src[i] = from;
+    a.dst[i] = to;
+  }
+  int total;
+  group_scan(refused, &total);
+  if (tid == 0) {
+    a.status[0] = total;
+    a.status[1] = max(0, need - found);
+  }
+}
+
+// Forks, second launch: workgroup i < n writes fork i's row, the others move
+// pages.
+__global__ __launch_bounds__(kThreads) void fork_kernel(TableArgs a, PageArgs pa) {
+  if (static_cast<int>(blockIdx.x) < a.n) {
+    const int i = blockIdx.x;
+    const int len = a.len[i];
+    if (len < 0) return;
+    const int full = len / a.page, to = a.dst[i];
+    const int32_t* from_row = a.tables + a.parents[i] * a.stride;
+    int32_t* row = a.tables + a.children[i] * a.stride;
+    for (int k = threadIdx.x; k < a.width; k += kThreads) {
+      int page = -1;
+      if (k < full) {
+        page = from_row[k];
+        atomicAdd(a.refs + page, 1);
+      } else if (k == full) {
+        page = to;
+      }
+      row[k] = page;
+    }
+    if (threadIdx.x == 0) a.lens[a.children[i]] = len;
+    return;
+  }
+  copy_pairs(pa, a.src, a.dst, a.n, blockIdx.x - a.n, gridDim.x - a.n);
+}
+
+// Compaction, first launch: the pages that move, where every page goes, and
+// the new reference counts.
+__global__ __launch_bounds__(kListThreads) void compact_list_kernel(TableArgs a) {
+  const int tid = threadIdx.x;
+  int mine = 0;
+  for (int p = tid; p < a.pages; p += kListThreads) mine += a.refs[p] > 0;
+  int live;
+  group_scan(mine, &live);
+  int holes = 0, movers = 0;
+  for (int p0 = 0; p0 < a.pages; p0 += kListThreads) {
+    const int p = p0 + tid;
+    const int used = p < a.pages && a.refs[p] > 0;
+    const int hole = p < live && !used, mover = used && p >= live;
+    // Both counts in one scan: a chunk has at most 1024 of each.
+    int total;
+    const int at = group_scan(hole | (mover << 16), &total);
+    if (hole) a.dst[holes + (at & 0xffff)] = p;
+    if (mover) a.src[movers + (at >> 16)] = p;
+    if (p < a.pages) a.map[p] = p;
+    holes += total & 0xffff;
+    movers += total >> 16;
+  }
+  __syncthreads();
+  for (int i = tid; i < movers; i += kListThreads) {
+    const int from = a.src[i], to = a.dst[i];
+    a.map[from] = to;
+    a.refs[to] = a.refs[from];
+    a.refs[from] = 0;
+  }
+  if (tid == 0) {
+    *a.count = movers;
+    a.status[0] = 0;
+    a.status[1] = live;
+  }
+}
+
+// Compaction, second launch: workgroup i < slots rewrites row i, the others
+// move pages.
+__global__ __launch_bounds__(kThreads) void compact_kernel(TableArgs a, PageArgs pa) {
+  if (static_cast<int>(blockIdx.x) < a.slots) {
+    int32_t* row = a.tables + blockIdx.x * a.stride;
+    for (int k = threadIdx.x; k < a.width; k += kThreads) {
+      const int page = row[k];
+      if (page >= 0 && page < a.pages) row[k] = a.map[page];
+    }
+    return;
+  }
+  copy_pairs(pa, a.src, a.dst, *a.count, blockIdx.x - a.slots, gridDim.x - a.slots);
+}
+
+PageArgs page_args(const xq_kv& kv) {
+  PageArgs a;
+  const int eb = elem_bytes(kv.dtype);
+  a.base[0] = static_cast<uint8_t*>(kv.k);
+  a.base[1] = static_cast<uint8_t*>(kv.v);
+  const int64_t* strides[2] = {kv.k_stride, kv.v_stride};
+  a.rows_bytes = kv.dim * eb;
+  a.whole = kv.kv_heads * kv.page * a.rows_bytes;
+  for (int i = 0; i < 2; ++i) {
+    a.layer[i] = strides[i][0] * eb;
+    a.page[i] = strides[i][1] * eb;
+    a.head[i] = strides[i][2] * eb;
+    a.tok[i] = strides[i][3] * eb;
+    const int64_t h = strides[i][2], t = strides[i][3];
+    const bool by_head = (t == kv.dim || kv.page == 1) && (h == kv.page * kv.dim || kv.kv_heads == 1);
+    const bool by_token = (h == kv.dim || kv.kv_heads == 1) && (t == kv.kv_heads * kv.dim || kv.page == 1);
+    if (!by_head && !by_token) a.whole = 0;
+  }
+  a.layers = static_cast<int>(kv.layers);
+  a.kv_heads = static_cast<int>(kv.kv_heads);
+  a.page_tokens = static_cast<int>(kv.page);
+  a.pages = static_cast<int>(kv.pages);
+  // A workgroup moves at most 16 KB of a page (four 16-byte words a thread).
+  const int64_t bytes = kv.kv_heads * kv.page * a.rows_bytes;
+  a.pieces = static_cast<int>(std::clamp<int64_t>(bytes / (16 * 1024), 1, 64));
+  return a;
+}
+
+// Workgroups for at most n page moves.
+int64_t move_blocks(const PageArgs& a, int64_t n) {
+  return std::clamp<int64_t>(std::min<int64_t>(n, 1 << 20) * a.layers * 2 * a.pieces, 1, 256 * 8 * 4);
+}
+
+TableArgs table_args(const xq_kv& kv, int32_t* refs, int32_t* tables, int64_t slots, int64_t width,
+                     int64_t stride, int32_t* status, void* ws) {
+  TableArgs a = {};
+  a.refs = refs;
+  a.tables = tables;
+  a.status = status;
+  a.stride = stride;
+  a.slots = static_cast<int>(slots);
+  a.width = static_cast<int>(width);
+  a.pages = static_cast<int>(kv.pages);
+  a.page = static_cast<int>(kv.page);
+  int32_t* w = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kCounterRegion);
+  a.count = w;
+  w += 64;
+  a.map = w;
+  w += kv.pages;
+  const int64_t list = std::max(kv.pages, slots);
+  a.src = w;
+  w += list;
+  a.dst = w;
+  w += list;
+  a.len = w;
+  w += slots;
+  a.claim = w;
+  return a;
+}
+
+}  // namespace
+
+size_t cache_workspace_bytes(int64_t pages, int64_t slots) {
+  return kCounterRegion + 4 * static_cast<size_t>(64 + pages + 2 * std::max(pages, slots) + 2 * slots);
+}
+
+hipError_t launch_cache_copy(const xq_kv& kv, const int32_t* src, const int32_t* dst, int64_t n,
+                             hipStream_t stream) {
+  const PageArgs a = page_args(kv);
+  copy_kernel<<<dim3(static_cast<uint32_t>(move_blocks(a, n))), dim3(kThreads), 0, stream>>>(a, src, dst, n);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_free(const xq_kv& kv, int32_t* refs, int32_t* tables, int64_t slots,
+                             int64_t width, int64_t stride, int32_t* lens, const int32_t* rows,
+                             int64_t n, hipStream_t stream) {
+  free_kernel<<<dim3(static_cast<uint32_t>(n)), dim3(kThreads), 0, stream>>>(
+      refs, static_cast<int>(kv.pages), tables, static_cast<int>(slots), static_cast<int>(width),
+      stride, lens, rows);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_fork(const xq_kv& kv, int32_t* refs, int32_t* tables, int64_t slots,
+                             int64_t width, int64_t stride, int32_t* lens, const int32_t* parents,
+                             const int32_t* children, int64_t n, int32_t* status, void* ws,
+                             hipStream_t stream) {
+  TableArgs t = table_args(kv, refs, tables, slots, width, stride, status, ws);
+  t.lens = lens;
+  t.parents = parents;
+  t.children = children;
+  t.n = static_cast<int>(n);
+  fork_list_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || n == 0) return e;
+  const PageArgs a = page_args(kv);
+  fork_kernel<<<dim3(static_cast<uint32_t>(n + move_blocks(a, n))), dim3(kThreads), 0, stream>>>(t, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_compact(const xq_kv& kv, int32_t* refs, int32_t* tables, int64_t slots,
+                                int64_t width, int64_t stride, int32_t* status, void* ws,
+                                hipStream_t stream) {
+  const TableArgs t = table_args(kv, refs, tables, slots, width, stride, status, ws);
+  compact_list_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const PageArgs a = page_args(kv);
+  // At most half the pages move.
+  compact_kernel<<<dim3(static_cast<uint32_t>(slots + move_blocks(a, kv.pages / 2 + 1))), dim3(kThreads), 0,
+                   stream>>>(t, a);
+  return hipGetLastError();
+}
+
+}  // namespace xq

@@ -14,11 +14,17 @@
 #include <cstring>
 
 #include "../../include/xq.h"
+#include "xq_host.h"
 #include "xq_launch.h"
 
 namespace {
 
 thread_local char g_err[256] = "";
+
+}  // namespace
+
+namespace xq {
+namespace host {
 
 xq_status fail(xq_status s, const char* fmt, ...) {
   va_list ap;
@@ -33,11 +39,9 @@ xq_status ok() {
   return XQ_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 constexpr int kMaxDevices = 64;
 // 0 = not checked, 1 = gfx950, 2 = other architecture.
-std::atomic<int> g_dev_state[kMaxDevices];
+static std::atomic<int> g_dev_state[kMaxDevices];
 
 xq_status check_device() {
   int dev = -1;
@@ -55,19 +59,6 @@ xq_status check_device() {
   if (st != 1) return fail(XQ_E_DEVICE, "device %d is not gfx950", dev);
   return XQ_OK;
 }
-
-xq_status check_k(int64_t K, int64_t kmax) {
-  if (K < 256 || K % 256 != 0) return fail(XQ_E_SHAPE, "K=%lld not a positive multiple of 256", (long long)K);
-  if (kmax > 0 && K > kmax)
-    return fail(XQ_E_SHAPE, "K=%lld above the largest supported K=%lld", (long long)K, (long long)kmax);
-  return XQ_OK;
-}
-
-constexpr int64_t kMaxInt = 2147483647LL;
-// Row counts stay below 2^30 so that no 32-bit row index in a kernel can wrap.
-constexpr int64_t kMaxRows = 1LL << 30;
-constexpr int64_t kIdMaxPairs = 1LL << 20;  // (token, slot) pairs of one grouped product
-constexpr int64_t kIdMaxExperts = 1024;
 
 // A call that needs `need` bytes of caller workspace: a null or short
 // workspace is refused by name (shape stage), a misaligned one at the
@@ -91,6 +82,26 @@ xq_status launched(hipError_t e, const char* what) {
   if (e != hipSuccess) return fail(XQ_E_LAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
   return ok();
 }
+
+}  // namespace host
+}  // namespace xq
+
+namespace {
+
+using namespace xq::host;
+
+xq_status check_k(int64_t K, int64_t kmax) {
+  if (K < 256 || K % 256 != 0) return fail(XQ_E_SHAPE, "K=%lld not a positive multiple of 256", (long long)K);
+  if (kmax > 0 && K > kmax)
+    return fail(XQ_E_SHAPE, "K=%lld above the largest supported K=%lld", (long long)K, (long long)kmax);
+  return XQ_OK;
+}
+
+constexpr int64_t kMaxInt = 2147483647LL;
+// Row counts stay below 2^30 so that no 32-bit row index in a kernel can wrap.
+constexpr int64_t kMaxRows = 1LL << 30;
+constexpr int64_t kIdMaxPairs = 1LL << 20;  // (token, slot) pairs of one grouped product
+constexpr int64_t kIdMaxExperts = 1024;
 
 }  // namespace
 
