@@ -389,7 +389,8 @@ typedef struct {
  *           bases 16-byte aligned.
  *  tables   device int32, row b at tables + b * table_stride, table_width
  *           pages per row; lens device int32[seqs].
- *  heads a multiple of kv_heads, heads / kv_heads <= 256, seqs * kv_heads <= 2^20.
+ *  heads a multiple of kv_heads, heads / kv_heads <= 256, seqs * kv_heads <= 2^20;
+ *  k, and v, of one layer within 64 GiB.
  *  window in 0..2^30 (0: none), sinks in 0..2^30 (read only with a window).
  *  max_len in 1..2^30: no length is above it (longer ones are clamped); the split of
  *  the work is planned for it, the result of a given plan is the same from

@@ -23,8 +23,10 @@
 //    lanes cover a whole row) and turns the 8 x 8 block around with byte
 //    permutes. Both m and l belong to head l % 16, which is also the lane's
 //    column of O^T, so rescaling is local to the lane.
-// The next tile's K is asked for before this tile's softmax, its V right after
-// this tile's product, the page numbers one tile earlier.
+// The next tile's K is asked for right after this tile's S^T, its V right after
+// this tile's product, the page numbers one tile earlier. (Tiles two ahead, in
+// twice the registers, or K turned round in LDS after whole-row loads, were
+// both slower.)
 //
 // Precision: q and the weights p enter the 16-bit matrix instructions as sums
 // of pieces (each the rounded remainder of the one before). For a 16-bit
@@ -45,8 +47,7 @@ constexpr int kTile = 32;                   // tokens of a wave's step
 constexpr int kStep = kTile * kWaves;       // tokens of a workgroup's step
 constexpr int kHeadTile = 16;               // heads of one workgroup
 constexpr int kCounterStride = 32;          // ints: a 128-byte line per arrival counter
-constexpr int64_t kMaxSplitUnits = 768;     // 96 KiB of counters, at the same place in every plan
-constexpr int kMaxSplits = 256;
+constexpr int kMaxGroups = 768;             // workgroups that share: 96 KiB of counters in every plan
 constexpr int kWaitVm0 = 0x0f70;            // s_waitcnt vmcnt(0), others untouched
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -60,7 +61,10 @@ struct DecodeArgs {
   int32_t* count;
   int64_t q_row, q_head, out_row, out_head;  // bytes
   int64_t table_stride, table_tokens;        // table_width * page
-  int kv_heads, group, dim, io, max_len, window, sinks, chunk, splits, head_tiles;
+  uint32_t k_page16, k_tok16, v_page16, v_tok16;  // in 16-byte units
+  int kv_heads, group, dim, max_len, window, sinks, seqs, head_tiles;
+  int shared;     // workgroups share all the work evenly; else one takes one unit
+  FastDiv ranges;  // parts that the sequences' steps are shared out to
   float c;        // scale * k_scale * log2(e)
   float v_scale;
 };
@@ -75,99 +79,122 @@ __device__ __forceinline__ float heads_sum(float v) {
   return v + __shfl_xor(v, 32, kWave);
 }
 
+// V's loads are whole rows that nothing reads again: non-temporal ones take
+// 131072 tokens x 2 from 190 to 174 us. K's take part of a row's line each, and
+// lose by it (32768 tokens x 8 stored token by token, 88 against 103 us).
 template <int BYTES>
 __device__ __forceinline__ u32x4 load_words(const uint8_t* p) {
   if constexpr (BYTES == 16) {
-    return *reinterpret_cast<const u32x4*>(p);
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
   } else if constexpr (BYTES == 8) {
-    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
     return u32x4{v.x, v.y, 0, 0};
   } else {
-    return u32x4{*reinterpret_cast<const uint32_t*>(p), 0, 0, 0};
+    return u32x4{__builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)), 0, 0, 0};
   }
 }
 
-// CT: the cache's type. DP: dim rounded up to 64, 128, 192 or 256. NQ, NP:
-// pieces of q and of p.
-template <int CT, int DP, int NQ, int NP>
-__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kernel(DecodeArgs a) {
+// Workgroups that a CU is given, its SIMDs one wave of each. Twice as many of
+// 128 dims and more, each with half the work, are slower: 131072 tokens x 2
+// 195 against 174 us, 64 windows of 8192 147 against 138; of 64 dims they are
+// faster (115 -> 95 us).
+constexpr int groups_per_cu(int dp) { return dp == 64 ? 2 : 1; }
+
+// CT: the cache's type. IO: q's and out's. DP: dim rounded up to 64, 128, 192
+// or 256; FULL: dim is DP.
+template <int CT, int IO, int DP, bool FULL>
+__global__ __launch_bounds__(kThreads, groups_per_cu(DP)) void attn_decode_kernel(DecodeArgs a) {
   constexpr int MT = CT == kBF16 ? kBF16 : kF16;   // the matrix instruction's type
   constexpr int EB = CT == kE4M3 ? 1 : 2;
+  constexpr int IB = IO == kF32 ? 4 : 2;
+  // Pieces of q and of p.
+  constexpr int NQ = MT == kBF16 ? (IO == kBF16 ? 1 : 3) : (IO == kF32 ? 2 : 1);
+  constexpr int NP = MT == kBF16 && IO == kF32 ? 3 : 2;
   constexpr int QS = DP / 32;                      // instructions of S^T along dim
-  // One K load gives KL instructions their operand: an 8-bit row's 16 bytes
-  // are 16 dims, two instructions' worth.
+  // 16 bytes of K give KL instructions their operand: an 8-bit row's are 16
+  // dims, two instructions' worth.
   constexpr int KL = CT == kE4M3 ? 2 : 1;
-  constexpr int KN = QS / KL;
+  constexpr int KN = QS / KL;                      // K loads of a lane per token
   constexpr int VE = DP == 64 ? 4 : 8;             // dims of a lane's V load
   constexpr int VC = (DP + 16 * VE - 1) / (16 * VE);
   constexpr int OS = DP + 4;                       // floats of a joined row in LDS
   extern __shared__ float lds[];
+  __shared__ __attribute__((aligned(16))) uint32_t places[kWaves][2][kTile];
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int l16 = lane % 16, lg = lane / 16;
-  const int unit = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int ht = unit % a.head_tiles;
-  const int kvh = (unit / a.head_tiles) % a.kv_heads;
-  const int seq = unit / a.head_tiles / a.kv_heads;
+  const int per_seq = a.kv_heads * a.head_tiles;  // units of a sequence
+  // A sequence's visible tokens as one run: `ns` sinks, then lo .. n-1.
+  auto length_of = [&](int len) {
+    return static_cast<int>(min(static_cast<int64_t>(max(0, min(len, a.max_len))), a.table_tokens));
+  };
+  auto low_of = [&](int n) { return a.window && n > a.window ? n - a.window : 0; };
+  auto steps_of = [&](int n) {
+    const int lo = low_of(n);
+    return max(1, (n - lo + min(a.sinks, lo) + kStep - 1) / kStep);
+  };
+
+  // This workgroup's unit (kv head and 16 of its heads), and its part of every
+  // sequence's steps laid end to end: [at, stop), `at` lying in sequence `seq`,
+  // which begins at `seq0`. Workgroups next to each other have one part and the
+  // sequence's units: they walk over the same pages at the same time, and a
+  // page's heads, which are neighbours in memory, are read together.
+  const int unit = blockIdx.x % per_seq, range = blockIdx.x / per_seq;
+  int seq, n, steps, at, stop, seq0, each;
+  if (a.shared) {
+    // Every wave adds up the sequences' steps for itself, 64 sequences at a
+    // time; with more, the second pass stops where `at` lies.
+    int n_l, steps_l, begin_l, before = 0, chunk = 0;
+    auto add_up = [&](int b) {
+      n_l = b + lane < a.seqs ? length_of(a.lens[b + lane]) : 0;
+      steps_l = b + lane < a.seqs ? steps_of(n_l) : 0;
+      int x = steps_l;
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) {
+        const int y = __shfl_up(x, d, kWave);
+        if (lane >= d) x += y;
+      }
+      begin_l = before + x - steps_l;
+      before += __builtin_amdgcn_readlane(x, kWave - 1);
+    };
+    for (int b = 0; b < a.seqs; b += kWave) add_up(b);
+    const int all = before;
+    each = div_by(all + a.ranges.d - 1, a.ranges);
+    at = range * each;
+    stop = min(all, at + each);
+    if (at >= stop) return;
+    if (a.seqs > kWave) {
+      before = 0;
+      for (;; chunk += kWave) {
+        add_up(chunk);
+        if (before > at) break;
+      }
+    }
+    // The last lane whose sequence begins at or before `at`.
+    const int l = kWave - 1 - __builtin_clzll(__ballot(steps_l > 0 && begin_l <= at));
+    seq = chunk + l;
+    n = __builtin_amdgcn_readlane(n_l, l);
+    steps = __builtin_amdgcn_readlane(steps_l, l);
+    seq0 = __builtin_amdgcn_readlane(begin_l, l);
+  } else {
+    seq = range;
+    n = length_of(a.lens[seq]);
+    steps = steps_of(n);
+    at = seq0 = 0;
+    stop = each = steps;
+  }
+  const int ht = unit % a.head_tiles, kvh = unit / a.head_tiles;
   const int heads = min(kHeadTile, a.group - ht * kHeadTile);  // of this workgroup
   const int head0 = kvh * a.group + ht * kHeadTile;
 
-  // The visible tokens as one run: `ns` sinks, then lo .. n-1.
-  const int n = static_cast<int>(
-      min(static_cast<int64_t>(max(0, min(a.lens[seq], a.max_len))), a.table_tokens));
-  const int lo = a.window && n > a.window ? n - a.window : 0;
-  const int ns = min(a.sinks, lo);
-  const int nv = n - lo + ns;
-  const int n_splits = max(1, (nv + a.chunk - 1) / a.chunk);
-  if (split >= n_splits) return;
-  const int begin = split * a.chunk, end = min(nv, begin + a.chunk);
+  for (bool first = true; at < stop; first = false) {
+  const int begin_step = at - seq0, end_step = min(steps, stop - seq0);
+  const int lo = low_of(n), ns = min(a.sinks, lo);
+  const int begin = begin_step * kStep, end = min(n - lo + ns, end_step * kStep);
 
   const uint8_t* kb = a.kv.k + kvh * a.kv.k_head;
   const uint8_t* vb = a.kv.v + kvh * a.kv.v_head;
   const int32_t* table = a.tables + seq * a.table_stride;
-
-  // q as the B operand: head l16, dims of step s. An f16 operand is scaled by
-  // a power of two that brings the head's largest |q| to 2^14..2^15, so that
-  // no piece of an f32 or bf16 q leaves f16's range.
-  u32x4 qf[QS][NQ];
-  float qs = a.c;
-  {
-    float x[QS][8];
-    float top = 0.f;
-    const uint8_t* qr = a.q + seq * a.q_row + (head0 + l16) * a.q_head;
-#pragma unroll
-    for (int s = 0; s < QS; ++s) {
-      const int d0 = KL == 1 ? s * 32 + lg * 8 : (s / 2) * 64 + lg * 16 + (s % 2) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[s][e] = l16 < heads && d0 < a.dim ? load_as_f32(qr, a.io, d0 + e) : 0.f;
-        top = fmaxf(top, fabsf(x[s][e]));
-      }
-    }
-    float mul = 1.f;
-    if constexpr (MT == kF16) {
-      top = heads_max(top);
-      if (top > 0.f && top < INFINITY) {
-        const int e = ilogbf(top);
-        mul = ldexpf(1.f, min(127, 14 - e));
-        qs = a.c * ldexpf(1.f, max(-127, e - 14));
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < QS; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        float u = x[s][e] * mul, w = x[s][e + 1] * mul;
-#pragma unroll
-        for (int p = 0; p < NQ; ++p) {
-          const uint32_t h = pack2<MT>(u, w);
-          qf[s][p][e / 2] = h;
-          const f32x2 back = unpack2<MT>(h);
-          u -= back.x;
-          w -= back.y;
-        }
-      }
-  }
 
   const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
   f32x4 o[VC][VE];
@@ -177,51 +204,63 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
     for (int j = 0; j < VE; ++j) o[c][j] = zero4;
   float m = -INFINITY, l = 0.f;
 
-  // The page of this lane's token (l % 32) of a tile, and its place.
+  // The lanes look up a tile's tokens (lane l token l % 32) and leave their
+  // places, in 16-byte units, in the wave's corner of LDS. Lane l's K loads
+  // need those of tokens l % 16 and 16 + l % 16, its V loads those of 4g .. 4g+3
+  // and 16 + those.
   auto token_of = [&](int u) { return u < ns ? u : lo + (u - ns); };
   auto page_of = [&](int u0) {
     const int u = u0 + lane % kTile;
-    return u < end ? table[div_by(token_of(u), a.kv.page)] : -1;
+    const int page = table[u < end ? div_by(token_of(u), a.kv.page) : 0];
+    return u < end ? page : -1;
   };
-  int64_t koff, voff;
   uint32_t live;  // bit t: token t of the tile is there
+  uint32_t k_at = 0, v_at = 0;
   auto place = [&](int u0, int page) {
     const int u = u0 + lane % kTile;
     const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.kv.pages);
     const uint32_t j = token_of(u);
     const uint32_t slot = j - div_by(j, a.kv.page) * a.kv.page.d;
-    // A token that is not there reads page 0, which always is; its score is
-    // hidden and its v is cleared.
-    koff = ok ? page * a.kv.k_page + slot * a.kv.k_tok : 0;
-    voff = ok ? page * a.kv.v_page + slot * a.kv.v_tok : 0;
+    // A token that is not there reads what was read last in its stead, at
+    // first the start of page 0, which is always there; its score is hidden
+    // and its v is cleared.
+    k_at = ok ? page * a.k_page16 + slot * a.k_tok16 : k_at;
+    v_at = ok ? page * a.v_page16 + slot * a.v_tok16 : v_at;
+    places[wave][0][lane % kTile] = k_at;
+    places[wave][1][lane % kTile] = v_at;
     live = static_cast<uint32_t>(__ballot(ok));
   };
   u32x4 kr[2][KN], vr[VC][8];
   auto load_k = [&]() {
+    uint32_t at[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) at[t] = places[wave][0][t * 16 + l16];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const uint8_t* p = kb + __shfl(koff, t * 16 + l16, kWave);
+      const uint8_t* p = kb + static_cast<uint64_t>(at[t]) * 16;
 #pragma unroll
       for (int s = 0; s < KN; ++s) {
         const int d0 = s * 32 * KL + lg * 8 * KL;
-        kr[t][s] = u32x4{0, 0, 0, 0};
-        if (d0 < a.dim) kr[t][s] = load_words<16>(p + d0 * EB);
+        kr[t][s] = *reinterpret_cast<const u32x4*>(p + (FULL || d0 < a.dim ? d0 : 0) * EB);
       }
     }
   };
   auto load_v = [&]() {
+    u32x4 at[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      at[t] = *reinterpret_cast<const u32x4*>(&places[wave][1][t * 16 + lg * 4]);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      const uint8_t* p = vb + __shfl(voff, (t / 4) * 16 + lg * 4 + t % 4, kWave);
+      const uint8_t* p = vb + static_cast<uint64_t>(at[t / 4][t % 4]) * 16;
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
+        // Dims past the end are read from the start; nothing uses them.
         const int d0 = (c * 16 + l16) * VE;
-        vr[c][t] = u32x4{0, 0, 0, 0};
-        if (d0 < a.dim) vr[c][t] = load_words<VE * EB>(p + d0 * EB);
+        vr[c][t] = load_words<VE * EB>(p + (FULL || d0 < a.dim ? d0 : 0) * EB);
       }
     }
   };
-
   auto widen_v = [&](const u32x4(&r)[8], u32x4(&w)[8]) {
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
@@ -243,39 +282,108 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
   };
 
   int u0 = begin + wave * kTile;
-  int page = -1;
-  if (u0 < end) {
-    page = page_of(u0);
-    place(u0, page);
-    page = page_of(u0 + kStep);
-    load_k();
-    load_v();
+  int page;  // of the lane's token in the next tile
+  // q as the B operand: head l16, dims of step s. An f16 operand is scaled by
+  // a power of two that brings the head's largest |q| to 2^14..2^15, so that
+  // no piece of an f32 or bf16 q leaves f16's range.
+  u32x4 qf[QS][NQ];
+  float qs = a.c;
+  {
+    float x[QS][8];
+    float top = 0.f;
+    const uint8_t* qr = a.q + seq * a.q_row + (head0 + l16) * a.q_head;
+    auto q_dim = [&](int s) {
+      return KL == 1 ? s * 32 + lg * 8 : (s / 2) * 64 + lg * 16 + (s % 2) * 8;
+    };
+    u32x4 raw[QS][IB / 2];
+#pragma unroll
+    for (int s = 0; s < QS; ++s) {
+      const bool in = l16 < heads && (FULL || q_dim(s) < a.dim);
+#pragma unroll
+      for (int i = 0; i < IB / 2; ++i) {
+        raw[s][i] = load_words<16>(in ? qr + q_dim(s) * IB + i * 16 : a.q);
+        if (!in) raw[s][i] = u32x4{0, 0, 0, 0};
+      }
+    }
+    // The first tile's loads go out behind q's, before q is waited for.
+    if (u0 < end) {
+      page = page_of(u0);
+      const int next = page_of(u0 + kStep);
+      place(u0, page);
+      page = next;
+      load_k();
+      load_v();
+    }
+#pragma unroll
+    for (int s = 0; s < QS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        f32x2 y;
+        if constexpr (IO == kF32) {
+          const uint32_t y0 = raw[s][e / 4][e % 4], y1 = raw[s][e / 4][e % 4 + 1];
+          y = f32x2{__builtin_bit_cast(float, y0), __builtin_bit_cast(float, y1)};
+        } else {
+          y = unpack2<IO>(raw[s][0][e / 2]);
+        }
+        x[s][e] = y.x;
+        x[s][e + 1] = y.y;
+        top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+      }
+    float mul = 1.f;
+    if constexpr (MT == kF16) {
+      top = heads_max(top);
+      if (top > 0.f && top < INFINITY) {
+        const int e = min(__builtin_amdgcn_frexp_expf(top), 126) - 15;
+        mul = ldexpf(1.f, min(127, -e));
+        qs = a.c * ldexpf(1.f, max(-127, e));
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < QS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        float u = x[s][e] * mul, w = x[s][e + 1] * mul;
+#pragma unroll
+        for (int p = 0; p < NQ; ++p) {
+          const uint32_t h = pack2<MT>(u, w);
+          qf[s][p][e / 2] = h;
+          const f32x2 back = unpack2<MT>(h);
+          u -= back.x;
+          w -= back.y;
+        }
+      }
   }
+
+  // The loads of the next tile are not conditional (past the last, its tokens
+  // are not there and read what was read before): the compiler then knows how
+  // many are under way and waits for no more than it needs.
   while (u0 < end) {  // wave-uniform
     const uint32_t here = live;
-    const int next = u0 + kStep;
-    if (next < end) {
-      place(next, page);
-      page = page_of(next + kStep);
-    }
-
     f32x4 st[2] = {zero4, zero4};
 #pragma unroll
     for (int s = 0; s < QS; ++s)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        u32x4 kf;
-        if constexpr (KL == 2) {
-          const u32x4 w = kr[t][s / 2];
-          const u32x2 x = widen4<MT>(w[(s % 2) * 2]), y = widen4<MT>(w[(s % 2) * 2 + 1]);
-          kf = u32x4{x.x, x.y, y.x, y.y};
-        } else {
-          kf = kr[t][s];
-        }
+      for (int p = 0; p < NQ; ++p)
 #pragma unroll
-        for (int p = 0; p < NQ; ++p) st[t] = mfma16<MT>(kf, qf[s][p], st[t]);
-      }
-    if (next < end) load_k();
+        for (int t = 0; t < 2; ++t) {
+          u32x4 kf;
+          if constexpr (KL == 2) {
+            const u32x4 w = kr[t][s / 2];
+            const u32x2 x = widen4<MT>(w[(s % 2) * 2]), y = widen4<MT>(w[(s % 2) * 2 + 1]);
+            kf = u32x4{x.x, x.y, y.x, y.y};
+          } else {
+            kf = kr[t][s];
+          }
+          if constexpr (!FULL) {
+            // q is 0 past the end, but 0 * infinity is not.
+            const int d0 = KL == 1 ? s * 32 + lg * 8 : (s / 2) * 64 + lg * 16 + (s % 2) * 8;
+            if (d0 >= a.dim) kf = u32x4{0, 0, 0, 0};
+          }
+          st[t] = mfma16<MT>(kf, qf[s][p], st[t]);
+        }
+    place(u0 + kStep, page);
+    page = page_of(u0 + 2 * kStep);
+    load_k();
 
     float s[8];
     float top = -INFINITY;
@@ -381,8 +489,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
         }
       }
     }
-    if (next < end) load_v();
-    u0 = next;
+    load_v();
+    u0 += kStep;
   }
 
   // Join the waves: LDS rows [wave][head] of o, then m and l.
@@ -409,8 +517,12 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
   __syncthreads();
 
   constexpr float kPScale = MT == kF16 ? 1.f / 16384.f : 1.f;
-  const bool whole = n_splits == 1;
-  float* po = a.part + (static_cast<int64_t>(unit) * a.splits) * kHeadTile * (DP + 2);
+  constexpr int PR = DP + 4;  // floats of a partial result per head: o, m, l, two of padding
+  const bool whole = begin_step == 0 && end_step == steps;
+  // A workgroup has at most two parts of sequences that it shares: its first
+  // and its last.
+  const int64_t part_size = static_cast<int64_t>(min(kHeadTile, a.group)) * PR;
+  float* mine = a.part + (2 * blockIdx.x + (first ? 0 : 1)) * part_size;
   for (int i = tid; i < heads * DP; i += kThreads) {
     const int r = i / DP, d = i % DP;
     float top = -INFINITY;
@@ -427,10 +539,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
     x *= kPScale;
     if (whole) {
       if (d < a.dim)
-        store_from_f32(a.out + seq * a.out_row + (head0 + r) * a.out_head, a.io, d,
+        store_from_f32(a.out + seq * a.out_row + (head0 + r) * a.out_head, IO, d,
                        sum == 0.f ? 0.f : x / sum * a.v_scale);
     } else {
-      float* mine = po + split * heads * (DP + 2);
       __hip_atomic_store(mine + i, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       if (d == 0) {
         __hip_atomic_store(mine + heads * DP + r, top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -439,114 +550,170 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
       }
     }
   }
-  if (whole) return;
 
-  // The last split to arrive joins them all. The partials and the counter are
-  // agent-scope atomics, which bypass the per-XCD L2's non-coherent state; each
-  // wave waits for its stores' acknowledgement before the barrier, so whoever
-  // sees the last count sees every partial.
-  __shared__ int last;
-  __builtin_amdgcn_s_waitcnt(kWaitVm0);
-  __syncthreads();
-  if (tid == 0)
-    last = __hip_atomic_fetch_add(a.count + static_cast<int64_t>(unit) * kCounterStride, 1,
-                                  __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n_splits - 1;
-  __syncthreads();
-  if (!last) return;  // workgroup-uniform
-  if (tid == 0)
-    __hip_atomic_store(a.count + static_cast<int64_t>(unit) * kCounterStride, 0, __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-  // Each split's factor per head, exp(m - max m) / sum, in LDS.
-  for (int r = wave; r < heads; r += kWaves) {
-    float sm[kMaxSplits / kWave], sl[kMaxSplits / kWave];
-    float top = -INFINITY;
+  if (!whole) {  // workgroup-uniform
+    // The ranges that hold the sequence's first and last step; the first one's
+    // counter counts, and its part is its second if it began with another one.
+    const int r0 = static_cast<uint32_t>(seq0) / static_cast<uint32_t>(each);
+    const int parts = static_cast<uint32_t>(seq0 + steps - 1) / static_cast<uint32_t>(each) - r0 + 1;
+    const int second = r0 * each < seq0;
+    const int g0 = r0 * per_seq + unit;
+    // The last part to arrive joins them all. The partials and the counter are
+    // agent-scope atomics, which bypass the per-XCD L2's non-coherent state;
+    // each wave waits for its stores' acknowledgement before the barrier, so
+    // whoever sees the last count sees every partial. It drops what its caches
+    // hold (the acquire fence) and reads them with plain 16-byte loads, several
+    // under way at once: read as atomics, 4 bytes at a time, 32 parts of 4
+    // heads took 18 us longer than 16.
+    __shared__ int last;
+    __builtin_amdgcn_s_waitcnt(kWaitVm0);
+    __syncthreads();
+    if (tid == 0)
+      last = __hip_atomic_fetch_add(a.count + g0 * kCounterStride, 1, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+    __syncthreads();
+    if (last) {  // workgroup-uniform
+      if (tid == 0)
+        __hip_atomic_store(a.count + g0 * kCounterStride, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      const float* p_first = a.part + (2 * g0 + second) * part_size;
+      const float* p_rest = a.part + 2 * g0 * part_size;  // part i > 0 is p_step * i on
+      const int64_t p_step = 2 * per_seq * part_size;
+      auto part = [&](int i) { return i ? p_rest + i * p_step : p_first; };
+      // A thread adds up four outputs over every `teams`th part, then the teams
+      // are added up. The first of its loads go out ahead of those that the
+      // factors wait for.
+      constexpr int kAhead = 8;
+      const int quads = heads * DP / 4, teams = max(1, kThreads / quads);
+      const int team = tid % teams;
+      f32x4 ahead[kAhead];
 #pragma unroll
-    for (int i = 0; i < kMaxSplits / kWave; ++i) {
-      const int sp = i * kWave + lane;
-      sm[i] = -INFINITY;
-      sl[i] = 0.f;
-      if (sp < n_splits) {
-        const float* p = po + sp * heads * (DP + 2) + heads * DP + r;
-        sm[i] = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        sl[i] = __hip_atomic_load(p + heads, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int k = 0; k < kAhead; ++k)
+        ahead[k] = reinterpret_cast<const f32x4*>(part(min(team + k * teams, parts - 1)))[min(tid / teams, quads - 1)];
+      // The parts' factors exp(m - max m) / sum, [head][part], in LDS.
+      for (int r = wave; r < heads; r += kWaves) {
+        const float* ml = part(min(lane, parts - 1)) + heads * DP + r;
+        const float m0 = lane < parts ? ml[0] : -INFINITY, l0 = ml[heads];
+        float top = m0;
+        for (int i = lane + kWave; i < parts; i += kWave) top = fmaxf(top, part(i)[heads * DP + r]);
+        top = wave_max(top);
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        for (int i = lane; i < parts; i += kWave) {
+          const float* p = part(i) + heads * DP + r;
+          const float f = exp2_fast((i < kWave ? m0 : p[0]) - base);
+          lds[r * parts + i] = f;
+          sum += f * (i < kWave ? l0 : p[heads]);
+        }
+        sum = wave_sum(sum);
+        const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+        for (int i = lane; i < parts; i += kWave) lds[r * parts + i] *= inv;
       }
-      top = fmaxf(top, sm[i]);
-    }
-    top = wave_max(top);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
+      __syncthreads();
+      f32x4* sums = reinterpret_cast<f32x4*>(lds + (heads * parts + 3) / 4 * 4);
+      for (int q0 = 0; q0 < quads; q0 += kThreads / teams) {
+        const int q = q0 + tid / teams, r = q * 4 / DP, d = q * 4 % DP;
+        f32x4 x = zero4;
+        if (q < quads) {
+          int i = team;
+          if (q0 == 0) {
 #pragma unroll
-    for (int i = 0; i < kMaxSplits / kWave; ++i) {
-      sm[i] = exp2_fast(sm[i] - base);
-      sum += sm[i] * sl[i];
-    }
-    sum = wave_sum(sum);
+            for (int k = 0; k < kAhead; ++k, i += teams)
+              if (i < parts) x += lds[r * parts + i] * ahead[k];
+          }
+#pragma unroll 8
+          for (; i < parts; i += teams)
+            x += lds[r * parts + i] * reinterpret_cast<const f32x4*>(part(i))[q];
+        }
+        if (teams > 1) {
+          sums[tid] = x;
+          __syncthreads();
+          if (team == 0)
+            for (int i = 1; i < teams; ++i) x += sums[tid + i];
+          __syncthreads();
+        }
+        if (team == 0 && q < quads && d < a.dim) {
 #pragma unroll
-    for (int i = 0; i < kMaxSplits / kWave; ++i) {
-      const int sp = i * kWave + lane;
-      if (sp < n_splits) lds[r * kMaxSplits + sp] = sum == 0.f ? 0.f : sm[i] / sum * a.v_scale;
+          for (int i = 0; i < 4; ++i)
+            store_from_f32(a.out + seq * a.out_row + (head0 + r) * a.out_head, IO, d + i, x[i]);
+        }
+      }
     }
   }
-  __syncthreads();
-  for (int i = tid; i < heads * DP; i += kThreads) {
-    const int r = i / DP, d = i % DP;
-    float x = 0.f;
-#pragma unroll 8
-    for (int sp = 0; sp < n_splits; ++sp)
-      x += lds[r * kMaxSplits + sp] * __hip_atomic_load(po + sp * heads * (DP + 2) + i,
-                                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (d < a.dim)
-      store_from_f32(a.out + seq * a.out_row + (head0 + r) * a.out_head, a.io, d, x);
+
+  // On to the next sequence.
+  at = seq0 = seq0 + steps;
+  if (at >= stop) break;
+  ++seq;
+  n = length_of(a.lens[seq]);
+  steps = steps_of(n);
+  __syncthreads();  // LDS is free again
   }
 }
 
 int dim_pad(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256; }
 
 struct Plan {
-  int64_t head_tiles, units, chunk, splits;
+  int64_t per_seq, ranges;  // units of a sequence; parts of all sequences' steps
+  bool shared;
 };
-// How many tokens a workgroup takes. The card holds 512 of these workgroups at
-// once; a split is worth its join from 128 tokens (one step) on.
+// As many workgroups as the card holds at once share the work evenly, to a
+// step: sequences of any lengths keep all of it busy to the end, at the price
+// of a join for each sequence that crosses from one range to the next. With
+// three and more units for each such workgroup, one unit each is even enough.
 Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t window,
           int64_t sinks) {
   Plan p;
   const int64_t group = heads / kv.kv_heads;
-  p.head_tiles = (group + kHeadTile - 1) / kHeadTile;
-  p.units = seqs * kv.kv_heads * p.head_tiles;
+  p.per_seq = kv.kv_heads * ((group + kHeadTile - 1) / kHeadTile);
   const int64_t most = window && window + sinks < max_len ? window + sinks : max_len;
-  const int64_t want = p.units > kMaxSplitUnits ? 1 : std::max<int64_t>(1, 1024 / p.units);
-  int64_t chunk = (most + want - 1) / want;
-  chunk = std::max<int64_t>(chunk, want == 1 ? most : (most + kMaxSplits - 1) / kMaxSplits);
-  p.chunk = std::max<int64_t>(1, (chunk + kStep - 1) / kStep) * kStep;
-  p.splits = (most + p.chunk - 1) / p.chunk;
+  const int64_t steps = (most + kStep - 1) / kStep;
+  const int64_t room = 256 * groups_per_cu(dim_pad(kv.dim));
+  p.shared = steps > 1 && seqs * p.per_seq < 3 * room && p.per_seq <= room && seqs * steps < (1 << 30);
+  p.ranges = p.shared ? std::min(room / p.per_seq, seqs * steps) : seqs;
   return p;
 }
 
-constexpr size_t kCounterBytes = kMaxSplitUnits * kCounterStride * 4;
+constexpr size_t kCounterBytes = static_cast<size_t>(kMaxGroups) * kCounterStride * 4;
 
-template <int CT, int DP, int NQ, int NP>
+template <int CT, int IO, int DP, bool FULL>
 hipError_t launch(const DecodeArgs& a, const Plan& p, hipStream_t stream) {
   const int heads = std::min(kHeadTile, a.group);
   size_t lds = static_cast<size_t>(kWaves) * heads * (DP + 4 + 2) * 4;
-  if (p.splits > 1) lds = std::max(lds, static_cast<size_t>(heads) * kMaxSplits * 4);
-  auto kernel = attn_decode_kernel<CT, DP, NQ, NP>;
-  if (lds > 64 * 1024) {
+  lds = std::max(lds, (static_cast<size_t>(heads) * (p.ranges + 1) + kThreads * 4 + 4) * 4);
+  auto kernel = attn_decode_kernel<CT, IO, DP, FULL>;
+  if (lds > 48 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(lds));
     if (e != hipSuccess) return e;
   }
-  kernel<<<dim3(static_cast<uint32_t>(p.units * p.splits)), dim3(kThreads), lds, stream>>>(a);
+  kernel<<<dim3(static_cast<uint32_t>(p.per_seq * p.ranges)), dim3(kThreads), lds, stream>>>(a);
   return hipGetLastError();
 }
 
-template <int CT, int NQ, int NP>
+template <int CT, int IO>
 hipError_t launch_dim(const DecodeArgs& a, const Plan& p, hipStream_t stream) {
+  switch (a.dim) {
+    case 64: return launch<CT, IO, 64, true>(a, p, stream);
+    case 128: return launch<CT, IO, 128, true>(a, p, stream);
+    case 192: return launch<CT, IO, 192, true>(a, p, stream);
+    case 256: return launch<CT, IO, 256, true>(a, p, stream);
+  }
   switch (dim_pad(a.dim)) {
-    case 64: return launch<CT, 64, NQ, NP>(a, p, stream);
-    case 128: return launch<CT, 128, NQ, NP>(a, p, stream);
-    case 192: return launch<CT, 192, NQ, NP>(a, p, stream);
-    default: return launch<CT, 256, NQ, NP>(a, p, stream);
+    case 64: return launch<CT, IO, 64, false>(a, p, stream);
+    case 128: return launch<CT, IO, 128, false>(a, p, stream);
+    case 192: return launch<CT, IO, 192, false>(a, p, stream);
+    default: return launch<CT, IO, 256, false>(a, p, stream);
+  }
+}
+
+template <int CT>
+hipError_t launch_io(int io, const DecodeArgs& a, const Plan& p, hipStream_t stream) {
+  switch (io) {
+    case kF32: return launch_dim<CT, kF32>(a, p, stream);
+    case kBF16: return launch_dim<CT, kBF16>(a, p, stream);
+    default: return launch_dim<CT, kF16>(a, p, stream);
   }
 }
 
@@ -555,9 +722,9 @@ hipError_t launch_dim(const DecodeArgs& a, const Plan& p, hipStream_t stream) {
 size_t attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len,
                                    int64_t window, int64_t sinks) {
   const Plan p = plan(seqs, heads, kv, max_len, window, sinks);
-  if (p.splits == 1) return 0;
-  return kCounterBytes + static_cast<size_t>(p.units) * p.splits * kHeadTile *
-                                (dim_pad(kv.dim) + 2) * 4;
+  if (!p.shared) return 0;
+  return kCounterBytes + static_cast<size_t>(p.per_seq * p.ranges) * 2 * std::min<int64_t>(kHeadTile, heads / kv.kv_heads) *
+                             (dim_pad(kv.dim) + 4) * 4;
 }
 
 hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t seqs, int64_t heads,
@@ -586,25 +753,23 @@ hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t se
   a.kv_heads = static_cast<int>(kv.kv_heads);
   a.group = static_cast<int>(heads / kv.kv_heads);
   a.dim = static_cast<int>(kv.dim);
-  a.io = q.type;
+  a.k_page16 = static_cast<uint32_t>(a.kv.k_page / 16);
+  a.k_tok16 = static_cast<uint32_t>(a.kv.k_tok / 16);
+  a.v_page16 = static_cast<uint32_t>(a.kv.v_page / 16);
+  a.v_tok16 = static_cast<uint32_t>(a.kv.v_tok / 16);
   a.max_len = static_cast<int>(max_len);
   a.window = static_cast<int>(window);
   a.sinks = static_cast<int>(sinks);
-  a.chunk = static_cast<int>(p.chunk);
-  a.splits = static_cast<int>(p.splits);
-  a.head_tiles = static_cast<int>(p.head_tiles);
+  a.seqs = static_cast<int>(seqs);
+  a.shared = p.shared;
+  a.ranges = fast_div(static_cast<uint32_t>(p.ranges));
+  a.head_tiles = static_cast<int>(p.per_seq / kv.kv_heads);
   a.c = scale * kv.k_scale * kLog2e;
   a.v_scale = kv.v_scale;
   switch (kv.dtype) {
-    case kBF16:
-      return q.type == kBF16 ? launch_dim<kBF16, 1, 2>(a, p, stream)
-                             : launch_dim<kBF16, 3, 3>(a, p, stream);
-    case kF16:
-      return q.type == kF32 ? launch_dim<kF16, 2, 2>(a, p, stream)
-                            : launch_dim<kF16, 1, 2>(a, p, stream);
-    default:
-      return q.type == kF32 ? launch_dim<kE4M3, 2, 2>(a, p, stream)
-                            : launch_dim<kE4M3, 1, 2>(a, p, stream);
+    case kBF16: return launch_io<kBF16>(q.type, a, p, stream);
+    case kF16: return launch_io<kF16>(q.type, a, p, stream);
+    default: return launch_io<kE4M3>(q.type, a, p, stream);
   }
 }
 

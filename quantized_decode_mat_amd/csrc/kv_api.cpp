@@ -77,6 +77,13 @@ xq_status check_attention(int64_t heads, const xq_kv* kv, float scale, int64_t w
   if (heads / kv->kv_heads > 256)
     return fail(XQ_E_SHAPE, "heads/kv_heads=%lld above 256", (long long)(heads / kv->kv_heads));
   if (!std::isfinite(scale)) return fail(XQ_E_SHAPE, "scale=%g not finite", scale);
+  for (const int64_t* st : {kv->k_stride, kv->v_stride}) {
+    // The kernels find a token by its place within a head, in 16-byte units.
+    const double last = static_cast<double>(kv->pages - 1) * static_cast<double>(st[1]) +
+                        static_cast<double>(kv->page - 1) * static_cast<double>(st[3]);
+    if (last * type_bytes(kv->dtype) >= 68719476736.0)
+      return fail(XQ_E_SHAPE, "kv pages of one layer reach over 64 GiB");
+  }
   if (window < 0 || window > kMaxLen)
     return fail(XQ_E_SHAPE, "window=%lld outside 0..2^30", (long long)window);
   if (sinks < 0 || sinks > kMaxLen)
