@@ -19,13 +19,12 @@
 //    its V operand comes from LDS by transposing loads (4 tokens of one dim
 //    per lane), in the same order of the summed index. O^T's column is again
 //    row l % 32: rescaling is local to the lane.
-// LDS rows are padded by 16 bytes, so 8 rows of a 16-byte column hit 32
-// different banks.
 //
 // Precision: S, the softmax and O are f32; q enters in its own 16 bits, an
 // 8-bit cache is widened exactly; p is rounded to 16 bits, as the product
 // needs.
 #include <algorithm>
+#include <cmath>
 
 #include "kv_device.h"
 #include "kv_launch.h"
@@ -50,7 +49,10 @@ struct PrefillArgs {
   int64_t table_stride, table_tokens;
   FastDiv group;
   int rows, seqs, kv_heads, dim, max_chunk, window, sinks, tiles;
-  float c, v_scale;
+  uint32_t k_page16, k_tok16, v_page16, v_tok16;  // in 16-byte units
+  int flip;       // q's sign is turned, for a negative scale
+  float c;        // |scale| * k_scale * log2(e)
+  float v_scale;
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -74,22 +76,41 @@ __device__ __forceinline__ float halves_max(float v) {
   const f32x2 s = both_halves(v);
   return fmaxf(s.x, s.y);
 }
+// Bits 0 .. n-1.
+__device__ __forceinline__ uint64_t below(int n) {
+  return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+// The largest of 16, or NaN if there is one: v_maximum3_f32. (fmaxf, which
+// drops NaN, would quiet each value first.)
+__device__ __forceinline__ float max16(f32x16 x) {
+  float r = x[0];
+#pragma unroll
+  for (int i = 1; i < 15; i += 2)
+    r = __builtin_elementwise_maximum(__builtin_elementwise_maximum(x[i], x[i + 1]), r);
+  return __builtin_elementwise_maximum(r, x[15]);
+}
 __device__ __forceinline__ float halves_sum(float v) {
   const f32x2 s = both_halves(v);
   return s.x + s.y;
 }
 
-// MT: q's and out's type. CT: the cache's, MT or kE4M3. DP: dim rounded up.
-template <int MT, int CT, int DP>
+// MT: q's and out's type. CT: the cache's, MT or kE4M3. DP: dim rounded up to
+// 64, 96, 128, 192 or 256; FULL: dim is DP.
+template <int MT, int CT, int DP, bool FULL>
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kernel(PrefillArgs a) {
   constexpr int EB = CT == kE4M3 ? 1 : 2;
-  constexpr int RB = DP * 2 + 16;            // bytes of a row in LDS
+  // Bytes of a row in LDS. A row of K begins 4 banks past the one before, so 8
+  // rows of a 16-byte column hit 32 banks; a row of V 8 banks (of 32 mod 128
+  // bytes), so the 4 rows x 32 bytes of a transposing load do.
+  constexpr int KB = DP * 2 + 16, VB = DP * 2 + 32;
+  constexpr int STAGE = kTile * (KB + VB);
   constexpr int CH = DP / 8;                 // 8-dim pieces of a row
   constexpr int PER = kTile * CH / kThreads; // of a thread, K and V each
   constexpr int DT = DP / 32;
   constexpr uint32_t kInf2 = MT == kBF16 ? 0x7f80u : 0x7c00u;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ int64_t offs[3][2][kTile];      // of a tile's tokens in k and v, -1: none
+  __shared__ uint32_t places[3][2][kTile];   // of a tile's tokens in k and v, in 16-byte units
+  __shared__ uint64_t found[3];              // bit t: token t of the tile is there
   __shared__ int odd[3];                     // a masked tile's V holds infinities or NaN
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
@@ -143,42 +164,52 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
       const int d0 = s * 16 + lh * 8;
       qf[s] = u32x4{0, 0, 0, 0};
       if (mine && d0 < a.dim) qf[s] = *reinterpret_cast<const u32x4*>(qr + d0 * 2);
+      if (a.flip) qf[s] ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
     }
   }
 
   const uint8_t* kb = a.kv.k + kvh * a.kv.k_head;
   const uint8_t* vb = a.kv.v + kvh * a.kv.v_head;
   const int32_t* table = a.tables + seq * a.table_stride;
-  // The first 64 threads look up a tile's tokens.
+  // The first wave looks up a tile's tokens. One that is not there reads the
+  // start of page 0, which always is; its score is hidden.
   auto page_of = [&](int t) {
-    const int j = tile_begin(t) + tid;
-    return t < tiles && tid < kTile && j < tile_end(t) ? table[div_by(j, a.kv.page)] : -1;
+    const int j = tile_begin(t) + lane;
+    const bool in = t < tiles && j < tile_end(t);
+    const int page = table[in ? div_by(j, a.kv.page) : 0];
+    return in ? page : -1;
   };
   auto place = [&](int t, int page) {
-    if (tid < kTile) {
-      const uint32_t j = tile_begin(t) + tid;
-      const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.kv.pages);
-      const uint32_t slot = j - div_by(j, a.kv.page) * a.kv.page.d;
-      offs[t % 3][0][tid] = ok ? page * a.kv.k_page + slot * a.kv.k_tok : -1;
-      offs[t % 3][1][tid] = ok ? page * a.kv.v_page + slot * a.kv.v_tok : -1;
-    }
+    const uint32_t j = tile_begin(t) + lane;
+    const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.kv.pages);
+    const uint32_t slot = j - div_by(j, a.kv.page) * a.kv.page.d;
+    places[t % 3][0][lane] = ok ? page * a.k_page16 + slot * a.k_tok16 : 0;
+    places[t % 3][1][lane] = ok ? page * a.v_page16 + slot * a.v_tok16 : 0;
+    const uint64_t all = __ballot(ok);
+    if (lane == 0) found[t % 3] = all;
   };
   u32x4 kr[PER], vr[PER];
-  auto load = [&](int t, int which, const uint8_t* from, u32x4(&reg)[PER]) {
+  auto load = [&](int t) {
+    uint32_t at[2][PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int at = tid + i * kThreads, row = at / CH, d0 = (at % CH) * 8;
-      const int64_t off = offs[t % 3][which][row];
-      reg[i] = u32x4{0, 0, 0, 0};
-      if (off >= 0 && d0 < a.dim) {
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) at[w][i] = places[t % 3][w][(tid + i * kThreads) / CH];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int d0 = (tid + i * kThreads) % CH * 8;
+        const uint8_t* p = (w ? vb : kb) + static_cast<uint64_t>(at[w][i]) * 16 +
+                           (FULL || d0 < a.dim ? d0 : 0) * EB;
+        u32x4& r = w ? vr[i] : kr[i];
         if constexpr (EB == 2) {
-          reg[i] = *reinterpret_cast<const u32x4*>(from + off + d0 * 2);
+          r = *reinterpret_cast<const u32x4*>(p);
         } else {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(from + off + d0);
-          reg[i] = u32x4{w.x, w.y, 0, 0};
+          const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+          r = u32x4{x.x, x.y, 0, 0};
         }
       }
-    }
   };
   auto widen = [&](u32x4 w) {
     if constexpr (EB == 2) {
@@ -196,25 +227,34 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     return true;
   };
   auto put = [&](int t) {
-    uint8_t* kl = smem + (t % 2) * (2 * kTile * RB);
-    uint8_t* vl = kl + kTile * RB;
-    const bool all = plain_tile(t);
+    uint8_t* kl = smem + (t % 2) * STAGE;
+    uint8_t* vl = kl + kTile * KB;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = tid + i * kThreads, row = at / CH, c = at % CH;
-      *reinterpret_cast<u32x4*>(kl + row * RB + c * 16) = widen(kr[i]);
-      u32x4 w = widen(vr[i]);
-      if (!all) {
-        // 0 * infinity must not reach a row that does not see the token: such
-        // values are left out here and added to the rows that do.
+      u32x4 w = widen(kr[i]);
+      // q is 0 past the end, but 0 * infinity is not.
+      if (!FULL && c * 8 >= a.dim) w = u32x4{0, 0, 0, 0};
+      *reinterpret_cast<u32x4*>(kl + row * KB + c * 16) = w;
+      vr[i] = widen(vr[i]);
+    }
+    if (!plain_tile(t) || found[t % 3] != ~0ull) {
+      // 0 * infinity must not reach a row that does not see the token: such
+      // values are left out here and added to the rows that do.
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool x = (w[e] & kInf2) == kInf2, y = ((w[e] >> 16) & kInf2) == kInf2;
+          const uint32_t w = vr[i][e];
+          const bool x = (w & kInf2) == kInf2, y = ((w >> 16) & kInf2) == kInf2;
           if (x || y) odd[t % 3] = 1;
-          w[e] &= (x ? 0u : 0xffffu) | (y ? 0u : 0xffff0000u);
+          vr[i][e] = w & ((x ? 0u : 0xffffu) | (y ? 0u : 0xffff0000u));
         }
-      }
-      *reinterpret_cast<u32x4*>(vl + row * RB + c * 16) = w;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = tid + i * kThreads, row = at / CH, c = at % CH;
+      *reinterpret_cast<u32x4*>(vl + row * VB + c * 16) = vr[i];
     }
   };
 
@@ -223,105 +263,153 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  // Weights are exp2(c s - ref). ref follows the row's maximum from below, by
+  // at most kLag: a weight is then at most 2^kLag, which neither its 16 bits
+  // nor the f32 sums mind, and the sums are hardly ever rescaled. `limit` is
+  // ref + kLag, or -infinity before the row's first token.
+  constexpr float kLag = 8.f;
+  float ref = 0.f, limit = -INFINITY, l = 0.f;
 
   if (tid < 3) odd[tid] = 0;
-  place(0, page_of(0));
-  place(1, page_of(1));
+  if (wave == 0) {
+    place(0, page_of(0));
+    place(1, page_of(1));
+  }
   __syncthreads();
   if (tiles > 0) {
-    load(0, 0, kb, kr);
-    load(0, 1, vb, vr);
+    load(0);
     put(0);
   }
   __syncthreads();
 
   for (int t = 0; t < tiles; ++t) {
-    const int page = page_of(t + 2);
+    int page = -1;
+    if (wave == 0) page = page_of(t + 2);
     if (tid == 0) odd[(t + 2) % 3] = 0;  // last read before the barrier, next set after the coming one
-    if (t + 1 < tiles) {
-      load(t + 1, 0, kb, kr);
-      load(t + 1, 1, vb, vr);
-    }
-    const uint8_t* kl = smem + (t % 2) * (2 * kTile * RB);
-    const uint8_t* vl = kl + kTile * RB;
+    load(t + 1 < tiles ? t + 1 : t);
+    const uint8_t* kl = smem + (t % 2) * STAGE;
+    const uint8_t* vl = kl + kTile * KB;
 
     f32x16 st[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 16; ++i) st[h][i] = 0.f;
+    // K goes through registers GS steps of 16 dims at a time, the next group's
+    // reads under way while one is worked on. (The fences keep that order; left
+    // to itself the compiler waits for each read.)
+    constexpr int GS = 2, GN = DP / 16 / GS;
+    u32x4 kf[2][GS][2];
+    auto read_k = [&](int g) {
 #pragma unroll
-      for (int s = 0; s < DP / 16; ++s) {
-        const u32x4 kf = *reinterpret_cast<const u32x4*>(kl + (h * 32 + l32) * RB + (s * 16 + lh * 8) * 2);
-        st[h] = mfma32<MT>(kf, qf[s], st[h]);
-      }
+      for (int s = 0; s < GS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          kf[g % 2][s][h] = *reinterpret_cast<const u32x4*>(
+              kl + (h * 32 + l32) * KB + ((g * GS + s) * 16 + lh * 8) * 2);
+    };
+    read_k(0);
+#pragma unroll
+    for (int g = 0; g < GN; ++g) {
+      if (g + 1 < GN) read_k(g + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < GS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) st[h] = mfma32<MT>(kf[g % 2][s][h], qf[g * GS + s], st[h]);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    // V's operands for 16 tokens, read 16 tokens ahead.
+    u32x4 vf[2][DT];
+    auto read_v = [&](int s) {
+      const uint8_t* vp = vl + (16 * s + 4 * lh + (lane % 16) / 4) * VB +
+                          (16 * ((lane / 16) % 2) + (lane % 4) * 4) * 2;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const u32x2 x = load_transposed(vp + d * 64), y = load_transposed(vp + 8 * VB + d * 64);
+        vf[s % 2][d] = u32x4{x.x, x.y, y.x, y.y};
+      }
+    };
+    read_v(0);
+    __builtin_amdgcn_sched_barrier(0);
 
     // A tile whose pages are all there and that every row sees needs no mask.
     const int b = tile_begin(t), e = tile_end(t);
-    const uint64_t there = __ballot(offs[t % 3][0][lane] >= 0);
-    const bool masked = !plain_tile(t) || there != ~0ull;
-    float top = -INFINITY;
+    const uint64_t there = found[t % 3];
+    // Else bit k of `vis` says whether the lane's row sees the tile's token k.
+    uint64_t vis = ~0ull;
+    if (!plain_tile(t) || there != ~0ull) {
+      vis = there & below(min(pos + 1, e) - b) & (~below(from + 1 - b) | below(sinks - b));
+      const uint64_t mine = vis >> (4 * lh);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t bits = static_cast<uint32_t>(mine >> (32 * h));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x = st[h][i] * a.c;
-        if (masked) {
-          const int k = h * 32 + 8 * (i / 4) + 4 * lh + i % 4, j = b + k;
-          const bool sees = ((there >> k) & 1) && j < e && j <= pos && (j > from || j < sinks);
-          if (!sees) x = -INFINITY;
-        }
-        st[h][i] = x;
-        top = fmaxf(top, x);
+        for (int i = 0; i < 16; ++i)
+          if (!(bits & (1u << (8 * (i / 4) + i % 4)))) st[h][i] = -INFINITY;
       }
-    top = fmaxf(m, halves_max(top));
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float alpha = exp2_fast(m - ref);
-    m = top;
-    float sum = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        st[h][i] = exp2_fast(st[h][i] - ref);
-        sum += st[h][i];
+    }
+    const float top = halves_max(fmaxf(max16(st[0]), max16(st[1]))) * a.c;
+    if (__ballot(top > limit)) {
+      const float to = top > limit ? top : ref;
+      const float alpha = limit == -INFINITY ? 0.f : exp2_fast(ref - to);
+      if (top > limit) {
+        ref = to;
+        limit = to + kLag;
       }
-    l = l * alpha + sum;
-    if (__ballot(alpha != 1.f)) {
+      l *= alpha;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
     }
+    // The weights of 16 tokens are formed while the matrix instructions of the
+    // 16 before run.
+    float sums[4] = {0.f, 0.f, 0.f, 0.f};
+    u32x4 pf[2];
+    auto weigh = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const int k = (s % 2) * 8 + i;
+        const float x = exp2_fast(fmaf(st[s / 2][k], a.c, -ref));
+        const float y = exp2_fast(fmaf(st[s / 2][k + 1], a.c, -ref));
+        sums[i / 2] += x + y;
+        pf[s % 2][i / 2] = pack2<MT>(x, y);
+      }
+    };
+    weigh(0);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      u32x4 pf;
+      if (s < 3) read_v(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        pf[i] = pack2<MT>(st[s / 2][(s % 2) * 8 + 2 * i], st[s / 2][(s % 2) * 8 + 2 * i + 1]);
-      const uint8_t* vp = vl + (16 * s + 4 * lh + (lane % 16) / 4) * RB +
-                          (16 * ((lane / 16) % 2) + (lane % 4) * 4) * 2;
+      for (int d = 0; d < DT; ++d) o[d] = mfma32<MT>(vf[s % 2][d], pf[s % 2], o[d]);
+      if (s < 3) {
+        weigh(s + 1);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const u32x2 x = load_transposed(vp + d * 64), y = load_transposed(vp + 8 * RB + d * 64);
-        o[d] = mfma32<MT>(u32x4{x.x, x.y, y.x, y.y}, pf, o[d]);
+        for (int d = 0; d < DT; ++d) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x402, (28 + DT - 1) / DT, 0);
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
     if (odd[t % 3]) {
-      // Infinities and NaN of this tile, for the rows that see them.
+      // Infinities and NaN of this tile, for the rows that see them. (What the
+      // compiler knows of this lane's dims it would work out ahead of the loop
+      // over tiles, and keep in registers that there are none of.)
+      int first_dim = 4 * lh;
+      asm volatile("" : "+v"(first_dim));
       for (int k = 0; k < kTile; ++k) {
-        const int64_t off = offs[t % 3][1][k];
-        const int j = b + k;
-        if (off < 0) continue;
-        const bool sees = j < e && j <= pos && (j > from || j < sinks);
+        const int64_t off = static_cast<int64_t>(places[t % 3][1][k]) * 16;
+        const bool sees = (vis >> k) & 1;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int dim = d * 32 + 8 * (i / 4) + 4 * lh + i % 4;
-            if (sees && dim < a.dim) {
+            const int dim = d * 32 + 8 * (i / 4) + first_dim + i % 4;
+            if (sees && (FULL || dim < a.dim)) {
               float x;
               if constexpr (EB == 2) {
                 x = load_as_f32(vb + off, MT, dim);
@@ -330,12 +418,13 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
               }
               if (!(fabsf(x) < INFINITY)) o[d][i] += x;
             }
+            if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few loads under way: registers are short
           }
       }
     }
 
     if (t + 1 < tiles) put(t + 1);
-    if (t + 2 < tiles) place(t + 2, page);
+    if (wave == 0) place(t + 2, page);
     __syncthreads();
   }
 
@@ -359,11 +448,11 @@ int64_t row_tiles(int64_t heads, const xq_kv& kv, int64_t max_chunk) {
   return (max_chunk * (heads / kv.kv_heads) + kRows - 1) / kRows;
 }
 
-template <int MT, int CT, int DP>
+template <int MT, int CT, int DP, bool FULL>
 hipError_t launch(const PrefillArgs& a, uint32_t blocks, hipStream_t stream) {
-  constexpr int lds = 2 * 2 * kTile * (DP * 2 + 16);
-  auto kernel = attn_prefill_kernel<MT, CT, DP>;
-  if (lds > 64 * 1024) {
+  constexpr int lds = 2 * kTile * (2 * DP * 2 + 48);
+  auto kernel = attn_prefill_kernel<MT, CT, DP, FULL>;
+  if (lds > 48 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
@@ -372,13 +461,19 @@ hipError_t launch(const PrefillArgs& a, uint32_t blocks, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int MT, int CT, int DP>
+hipError_t launch_full(const PrefillArgs& a, uint32_t blocks, hipStream_t stream) {
+  return a.dim == DP ? launch<MT, CT, DP, true>(a, blocks, stream)
+                     : launch<MT, CT, DP, false>(a, blocks, stream);
+}
+
 template <int MT, int CT>
 hipError_t launch_dim(const PrefillArgs& a, uint32_t blocks, hipStream_t stream) {
-  if (a.dim <= 64) return launch<MT, CT, 64>(a, blocks, stream);
-  if (a.dim <= 96) return launch<MT, CT, 96>(a, blocks, stream);
-  if (a.dim <= 128) return launch<MT, CT, 128>(a, blocks, stream);
-  if (a.dim <= 192) return launch<MT, CT, 192>(a, blocks, stream);
-  return launch<MT, CT, 256>(a, blocks, stream);
+  if (a.dim <= 64) return launch_full<MT, CT, 64>(a, blocks, stream);
+  if (a.dim <= 96) return launch_full<MT, CT, 96>(a, blocks, stream);
+  if (a.dim <= 128) return launch_full<MT, CT, 128>(a, blocks, stream);
+  if (a.dim <= 192) return launch_full<MT, CT, 192>(a, blocks, stream);
+  return launch_full<MT, CT, 256>(a, blocks, stream);
 }
 
 }  // namespace
@@ -418,7 +513,12 @@ hipError_t launch_attn_prefill(const RowsView& out, const RowsView& q, int64_t r
   a.window = static_cast<int>(window);
   a.sinks = static_cast<int>(sinks);
   a.tiles = static_cast<int>(row_tiles(heads, kv, max_chunk));
-  a.c = scale * kv.k_scale * kLog2e;
+  a.k_page16 = static_cast<uint32_t>(a.kv.k_page / 16);
+  a.k_tok16 = static_cast<uint32_t>(a.kv.k_tok / 16);
+  a.v_page16 = static_cast<uint32_t>(a.kv.v_page / 16);
+  a.v_tok16 = static_cast<uint32_t>(a.kv.v_tok / 16);
+  a.flip = scale < 0.f;
+  a.c = std::fabs(scale) * kv.k_scale * kLog2e;
   a.v_scale = kv.v_scale;
   const uint32_t blocks = static_cast<uint32_t>(attn_prefill_blocks(seqs, heads, kv, max_chunk));
   if (q.type == kBF16)
