@@ -229,6 +229,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
   auto put = [&](int t) {
     uint8_t* kl = smem + (t % 2) * STAGE;
     uint8_t* vl = kl + kTile * KB;
+    const bool masked = !plain_tile(t) || found[t % 3] != ~0ull;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = tid + i * kThreads, row = at / CH, c = at % CH;
@@ -236,25 +237,26 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
       // q is 0 past the end, but 0 * infinity is not.
       if (!FULL && c * 8 >= a.dim) w = u32x4{0, 0, 0, 0};
       *reinterpret_cast<u32x4*>(kl + row * KB + c * 16) = w;
-      vr[i] = widen(vr[i]);
-    }
-    if (!plain_tile(t) || found[t % 3] != ~0ull) {
-      // 0 * infinity must not reach a row that does not see the token: such
-      // values are left out here and added to the rows that do.
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t w = vr[i][e];
-          const bool x = (w & kInf2) == kInf2, y = ((w >> 16) & kInf2) == kInf2;
-          if (x || y) odd[t % 3] = 1;
-          vr[i][e] = w & ((x ? 0u : 0xffffu) | (y ? 0u : 0xffff0000u));
-        }
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = tid + i * kThreads, row = at / CH, c = at % CH;
-      *reinterpret_cast<u32x4*>(vl + row * VB + c * 16) = vr[i];
+      u32x4 w = widen(vr[i]);
+      if (masked) {
+        // 0 * infinity must not reach a row that does not see the token: such
+        // values are left out here and added to the rows that do.
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool x = (w[e] & kInf2) == kInf2, y = ((w[e] >> 16) & kInf2) == kInf2;
+          any |= x || y;
+          w[e] &= (x ? 0u : 0xffffu) | (y ? 0u : 0xffff0000u);
+        }
+        if (any) odd[t % 3] = 1;
+      }
+      *reinterpret_cast<u32x4*>(vl + row * VB + c * 16) = w;
+      // (Widened one after the other: registers are short.)
+      if constexpr (EB == 1) __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -308,6 +310,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
           kf[g % 2][s][h] = *reinterpret_cast<const u32x4*>(
               kl + (h * 32 + l32) * KB + ((g * GS + s) * 16 + lh * 8) * 2);
     };
+    __builtin_amdgcn_s_setprio(1);
     read_k(0);
 #pragma unroll
     for (int g = 0; g < GN; ++g) {
@@ -332,6 +335,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     };
     read_v(0);
     __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
 
     // A tile whose pages are all there and that every row sees needs no mask.
     const int b = tile_begin(t), e = tile_end(t);
@@ -374,10 +378,13 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
         const float x = exp2_fast(fmaf(st[s / 2][k], a.c, -ref));
         const float y = exp2_fast(fmaf(st[s / 2][k + 1], a.c, -ref));
         sums[i / 2] += x + y;
+        // (Here, beside the matrix instructions, not after them all.)
+        asm volatile("" : "+v"(sums[i / 2]));
         pf[s % 2][i / 2] = pack2<MT>(x, y);
       }
     };
     weigh(0);
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s < 3) read_v(s + 1);
@@ -394,6 +401,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
     l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
     if (odd[t % 3]) {
       // Infinities and NaN of this tile, for the rows that see them. (What the
