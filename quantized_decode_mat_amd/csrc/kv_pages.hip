@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kListThreads = 1024;
+constexpr int kRun = 8;  // pages in a row that a thread of the lists takes
 // The first bytes of a workspace are where other calls keep counters that
 // have to stay zero.
 constexpr size_t kCounterRegion = 96 * 1024;
@@ -144,6 +145,7 @@ struct TableArgs {
 // one.
 __global__ __launch_bounds__(kListThreads) void fork_list_kernel(TableArgs a) {
   const int tid = threadIdx.x;
+  __shared__ int parent[kListThreads], pages_of[kListThreads], bad[kListThreads];
   for (int i = tid; i < a.slots; i += kListThreads) a.claim[i] = a.n;
   __syncthreads();
   for (int i = tid; i < a.n; i += kListThreads) {
@@ -151,46 +153,67 @@ __global__ __launch_bounds__(kListThreads) void fork_list_kernel(TableArgs a) {
     if (c >= 0 && c < a.slots) atomicMin(a.claim + c, i);
   }
   __syncthreads();
-  // A wave checks a fork, its lanes the parent's pages.
-  const int lane = tid % kWave;
-  for (int i = tid / kWave; i < a.n; i += kListThreads / kWave) {
-    const int c = a.children[i], p = a.parents[i];
-    int len = -1;
-    if (c >= 0 && c < a.slots && p >= 0 && p < a.slots &&
-        __hip_atomic_load(a.claim + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == i &&
-        a.lens[c] == 0)
-      len = a.lens[p];
-    const int64_t pages = len < 0 ? 0 : (static_cast<int64_t>(len) + a.page - 1) / a.page;
-    if (pages > a.width) len = -1;
-    int bad = 0;
-    if (len > 0)
-      for (int k = lane; k < pages; k += kWave)
-        bad |= static_cast<uint32_t>(a.tables[p * a.stride + k]) >= static_cast<uint32_t>(a.pages);
-    if (__ballot(bad)) len = -1;
-    if (lane == 0) a.len[i] = len;
-  }
-  __syncthreads();
-  // How many fresh pages, and each fork's number among those that need one.
+  // 1024 forks at a time: which are sound, and the number of each among those
+  // that need a fresh page.
   int need = 0, refused = 0;
   for (int i0 = 0; i0 < a.n; i0 += kListThreads) {
     const int i = i0 + tid;
-    const int len = i < a.n ? a.len[i] : 0;
+    int len = -1;
+    pages_of[tid] = 0;
+    bad[tid] = 0;
+    if (i < a.n) {
+      const int c = a.children[i], p = a.parents[i];
+      if (c >= 0 && c < a.slots && p >= 0 && p < a.slots &&
+          __hip_atomic_load(a.claim + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == i) {
+        const int own = a.lens[c], of_parent = a.lens[p];
+        if (own == 0 && (static_cast<int64_t>(of_parent) + a.page - 1) / a.page <= a.width) len = of_parent;
+      }
+      if (len > 0) {
+        parent[tid] = p;
+        pages_of[tid] = static_cast<int>((static_cast<int64_t>(len) + a.page - 1) / a.page);
+      }
+    }
+    __syncthreads();
+    // All the parents' pages, entry by entry.
+    const int64_t entries = static_cast<int64_t>(min(kListThreads, a.n - i0)) * a.width;
+#pragma unroll 4
+    for (int64_t k = tid; k < entries; k += kListThreads) {
+      const int f = static_cast<int>(k / a.width), e = static_cast<int>(k - static_cast<int64_t>(f) * a.width);
+      if (e < pages_of[f] &&
+          static_cast<uint32_t>(a.tables[parent[f] * a.stride + e]) >= static_cast<uint32_t>(a.pages))
+        bad[f] = 1;
+    }
+    __syncthreads();
+    if (bad[tid]) len = -1;
     const int part = len > 0 && len % a.page > 0;
-    refused += len < 0;
+    refused += i < a.n && len < 0;
     int total;
     const int at = need + group_scan(part, &total);
-    if (i < a.n) a.src[i] = part ? at : -1;
+    if (i < a.n) {
+      a.len[i] = len;
+      a.src[i] = part ? at : -1;
+    }
     need += total;
   }
   __syncthreads();
-  // The first `need` free pages, ascending, into dst by number.
+  // The first `need` free pages, ascending, into the map by number; a thread
+  // takes kRun pages in a row.
   int found = 0;
-  for (int p0 = 0; p0 < a.pages && found < need; p0 += kListThreads) {
-    const int p = p0 + tid;
-    const int is_free = p < a.pages && a.refs[p] == 0;
+  for (int64_t p0 = 0; p0 < a.pages && found < need; p0 += kListThreads * kRun) {
+    const int64_t p = p0 + tid * kRun;
+    int ref[kRun], mine = 0;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) ref[k] = p + k < a.pages ? a.refs[p + k] : 1;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) mine += ref[k] == 0;
     int total;
-    const int at = found + group_scan(is_free, &total);
-    if (is_free && at < need) a.map[at] = p;
+    int at = found + group_scan(mine, &total);
+#pragma unroll
+    for (int k = 0; k < kRun; ++k)
+      if (ref[k] == 0) {
+        if (at < need) a.map[at] = static_cast<int>(p + k);
+        ++at;
+      }
     found += total;
   }
   __syncthreads();
@@ -248,21 +271,47 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(TableArgs a, PageArgs pa
 // the new reference counts.
 __global__ __launch_bounds__(kListThreads) void compact_list_kernel(TableArgs a) {
   const int tid = threadIdx.x;
-  int mine = 0;
-  for (int p = tid; p < a.pages; p += kListThreads) mine += a.refs[p] > 0;
+  // A thread takes kRun pages in a row, of every kListThreads * kRun; the first
+  // such run stays in registers for the second pass.
+  int first[kRun], mine = 0;
+  auto load = [&](int64_t p, int(&ref)[kRun]) {
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) ref[k] = p + k < a.pages ? a.refs[p + k] : 0;
+  };
+  load(tid * kRun, first);
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) mine += first[k] > 0;
+  for (int64_t p0 = kListThreads * kRun; p0 < a.pages; p0 += kListThreads * kRun) {
+    int ref[kRun];
+    load(p0 + tid * kRun, ref);
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) mine += ref[k] > 0;
+  }
   int live;
   group_scan(mine, &live);
   int holes = 0, movers = 0;
-  for (int p0 = 0; p0 < a.pages; p0 += kListThreads) {
-    const int p = p0 + tid;
-    const int used = p < a.pages && a.refs[p] > 0;
-    const int hole = p < live && !used, mover = used && p >= live;
-    // Both counts in one scan: a chunk has at most 1024 of each.
+  for (int64_t p0 = 0; p0 < a.pages; p0 += kListThreads * kRun) {
+    const int64_t p = p0 + tid * kRun;
+    if (p0) load(p, first);
+    // Both counts in one scan: a round has at most 8192 of each.
+    int counts = 0;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const bool used = first[k] > 0;
+      counts += p + k >= a.pages ? 0 : p + k < live ? !used : used << 16;
+    }
     int total;
-    const int at = group_scan(hole | (mover << 16), &total);
-    if (hole) a.dst[holes + (at & 0xffff)] = p;
-    if (mover) a.src[movers + (at >> 16)] = p;
-    if (p < a.pages) a.map[p] = p;
+    const int at = group_scan(counts, &total);
+    int hole = holes + (at & 0xffff), mover = movers + (at >> 16);
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      if (p + k >= a.pages) continue;
+      const bool used = first[k] > 0;
+      const int page = static_cast<int>(p + k);
+      if (page < live && !used) a.dst[hole++] = page;
+      if (page >= live && used) a.src[mover++] = page;
+      a.map[page] = page;
+    }
     holes += total & 0xffff;
     movers += total >> 16;
   }
