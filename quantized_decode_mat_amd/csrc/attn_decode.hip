@@ -657,10 +657,12 @@ struct Plan {
   int64_t per_seq, ranges;  // units of a sequence; parts of all sequences' steps
   bool shared;
 };
-// As many workgroups as the card holds at once share the work evenly, to a
-// step: sequences of any lengths keep all of it busy to the end, at the price
-// of a join for each sequence that crosses from one range to the next. With
-// three and more units for each such workgroup, one unit each is even enough.
+// As many workgroups as fill the card share the work evenly, to a step:
+// sequences of any lengths keep all of it busy to the end, at the price of a
+// join (3.6 us) for each sequence that crosses from one range to the next. Up
+// to three steps (384 tokens) one workgroup is faster than a join: 300 tokens
+// take 10.4 against 11.2 us, 517 tokens 13 against 11.2. With three and more
+// units for each such workgroup, one unit each is even enough.
 Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t window,
           int64_t sinks) {
   Plan p;
@@ -669,7 +671,7 @@ Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t
   const int64_t most = window && window + sinks < max_len ? window + sinks : max_len;
   const int64_t steps = (most + kStep - 1) / kStep;
   const int64_t room = 256 * groups_per_cu(dim_pad(kv.dim));
-  p.shared = steps > 1 && seqs * p.per_seq < 3 * room && p.per_seq <= room && seqs * steps < (1 << 30);
+  p.shared = steps > 3 && seqs * p.per_seq < 3 * room && p.per_seq <= room && seqs * steps < (1 << 30);
   p.ranges = p.shared ? std::min(room / p.per_seq, seqs * steps) : seqs;
   return p;
 }
