@@ -64,6 +64,9 @@ struct DecodeArgs {
   uint32_t k_page16, k_tok16, v_page16, v_tok16;  // in 16-byte units
   int kv_heads, group, dim, max_len, window, sinks, seqs, head_tiles;
   int shared;     // workgroups share all the work evenly; else one takes one unit
+  const int32_t* starts;  // of a chunk's rows
+  int rows, max_chunk;
+  FastDiv group_div;
   FastDiv ranges;  // parts that the sequences' steps are shared out to
   float c;        // scale * k_scale * log2(e)
   float v_scale;
@@ -78,6 +81,9 @@ __device__ __forceinline__ float heads_sum(float v) {
   v += __shfl_xor(v, 16, kWave);
   return v + __shfl_xor(v, 32, kWave);
 }
+
+// Bits 0 .. n-1.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0 : n >= 32 ? ~0u : (1u << n) - 1; }
 
 // V's loads are whole rows that nothing reads again: non-temporal ones take
 // 131072 tokens x 2 from 190 to 174 us. K's take part of a row's line each, and
@@ -101,8 +107,10 @@ __device__ __forceinline__ u32x4 load_words(const uint8_t* p) {
 constexpr int groups_per_cu(int dp) { return dp == 64 ? 2 : 1; }
 
 // CT: the cache's type. IO: q's and out's. DP: dim rounded up to 64, 128, 192
-// or 256; FULL: dim is DP.
-template <int CT, int IO, int DP, bool FULL>
+// or 256; FULL: dim is DP. CHUNK: several new tokens per sequence; a
+// workgroup's 16 columns are then 16 of a sequence's (token, head) rows, which
+// see different tokens.
+template <int CT, int IO, int DP, bool FULL, bool CHUNK>
 __global__ __launch_bounds__(kThreads, groups_per_cu(DP)) void attn_decode_kernel(DecodeArgs a) {
   constexpr int MT = CT == kBF16 ? kBF16 : kF16;   // the matrix instruction's type
   constexpr int EB = CT == kE4M3 ? 1 : 2;
@@ -179,24 +187,52 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(DP)) void attn_decode_kerne
   } else {
     seq = range;
     n = length_of(a.lens[seq]);
-    steps = steps_of(n);
+    steps = CHUNK ? 1 : steps_of(n);
     at = seq0 = 0;
     stop = each = steps;
   }
   const int ht = unit % a.head_tiles, kvh = unit / a.head_tiles;
-  const int heads = min(kHeadTile, a.group - ht * kHeadTile);  // of this workgroup
-  const int head0 = kvh * a.group + ht * kHeadTile;
+  // This workgroup's heads, or rows: `heads` of them, the first head0. Row r of
+  // a chunk is its token r / group, and head r % group of the kv head's.
+  int heads, head0, first_row = 0, pos = 0, pmin = 0, pmax = 0;
+  if constexpr (CHUNK) {
+    first_row = min(max(a.starts[seq], 0), a.rows);
+    const int count = min(min(max(a.starts[seq + 1], first_row), a.rows) - first_row, a.max_chunk);
+    head0 = ht * kHeadTile;
+    heads = min(kHeadTile, count * a.group - head0);
+    if (heads <= 0) return;
+    pos = n - count + static_cast<int>(div_by(head0 + min(l16, heads - 1), a.group_div));
+    pmin = n - count + static_cast<int>(div_by(head0, a.group_div));
+    pmax = n - count + static_cast<int>(div_by(head0 + heads - 1, a.group_div));
+  } else {
+    heads = min(kHeadTile, a.group - ht * kHeadTile);
+    head0 = kvh * a.group + ht * kHeadTile;
+  }
+  const int sinks = a.window ? a.sinks : 0;
+  // Byte offset of this workgroup's row r, given a tensor's strides.
+  auto row_at = [&](int r, int64_t row_stride, int64_t head_stride) {
+    if constexpr (CHUNK) {
+      const int t = div_by(head0 + r, a.group_div);
+      return (first_row + t) * row_stride + (kvh * a.group + head0 + r - t * a.group) * head_stride;
+    } else {
+      return seq * row_stride + (head0 + r) * head_stride;
+    }
+  };
 
   for (bool first = true; at < stop; first = false) {
   const int begin_step = at - seq0, end_step = min(steps, stop - seq0);
-  const int lo = low_of(n), ns = min(a.sinks, lo);
-  const int begin = begin_step * kStep, end = min(n - lo + ns, end_step * kStep);
+  // The tokens that any row sees.
+  const int lo = CHUNK ? (a.window ? max(0, pmin - a.window + 1) : 0) : low_of(n), ns = min(sinks, lo);
+  const int begin = begin_step * kStep;
+  const int end = CHUNK ? max(0, pmax + 1 - lo) + ns : min(n - lo + ns, end_step * kStep);
 
   const uint8_t* kb = a.kv.k + kvh * a.kv.k_head;
   const uint8_t* vb = a.kv.v + kvh * a.kv.v_head;
   const int32_t* table = a.tables + seq * a.table_stride;
 
   const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
+  constexpr uint32_t kSigns = EB == 1 ? 0x80808080u : 0x80008000u;
+  constexpr uint32_t kOne = EB == 1 ? 0x01010101u : CT == kBF16 ? 0x00800080u : 0x04000400u;
   f32x4 o[VC][VE];
 #pragma unroll
   for (int c = 0; c < VC; ++c)
@@ -291,7 +327,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(DP)) void attn_decode_kerne
   {
     float x[QS][8];
     float top = 0.f;
-    const uint8_t* qr = a.q + seq * a.q_row + (head0 + l16) * a.q_head;
+    const uint8_t* qr = a.q + row_at(min(l16, heads - 1), a.q_row, a.q_head);
     auto q_dim = [&](int s) {
       return KL == 1 ? s * 32 + lg * 8 : (s / 2) * 64 + lg * 16 + (s % 2) * 8;
     };
@@ -385,12 +421,29 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(DP)) void attn_decode_kerne
     page = page_of(u0 + 2 * kStep);
     load_k();
 
+    // Which of the tile's tokens this lane's row sees.
+    uint32_t sees = here;
+    bool same = true;  // for all rows
+    if constexpr (CHUNK) {
+      const int u = u0;
+      const int j0 = token_of(u), j31 = token_of(u + kTile - 1);
+      same = j31 <= pmin && (!a.window || j0 > pmax - a.window || j31 < sinks);
+      if (!same) {
+        // Bit k is token u + k where that is a sink, else token j + k.
+        const int j = lo + u - ns;
+        const uint32_t sink = below(ns - u) & below(pos + 1 - u);
+        const uint32_t rest = ~below(ns - u) & below(pos + 1 - j) &
+                              (a.window ? ~below(pos - a.window + 1 - j) | below(sinks - j) : ~0u);
+        sees = sink | rest;
+        sees &= here;
+      }
+    }
     float s[8];
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       s[i] = st[i / 4][i % 4] * qs;
-      if (!((here >> ((i / 4) * 16 + lg * 4 + i % 4)) & 1)) s[i] = -INFINITY;
+      if (!((sees >> ((i / 4) * 16 + lg * 4 + i % 4)) & 1)) s[i] = -INFINITY;
       top = fmaxf(top, s[i]);
     }
     top = fmaxf(m, heads_max(top));
@@ -437,20 +490,60 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(DP)) void attn_decode_kerne
 #pragma unroll
           for (int c = 0; c < VC; ++c) vr[c][t] = u32x4{0, 0, 0, 0};
     }
-    // Whether the tile's V has an infinity or NaN: an exponent of all ones
-    // carries into the sign's place. (An 8-bit V has no infinity, and NaN needs
-    // no care.)
+    // Whether the tile's V has an infinity or NaN: an exponent of all ones (of
+    // 8 bits, all ones but the sign) carries into the sign's place. (An 8-bit V
+    // has no infinity, and a NaN that every row sees needs no care.)
     bool odd = false;
-    if constexpr (CT != kE4M3) {
-      constexpr uint32_t kOne = CT == kBF16 ? 0x00800080u : 0x04000400u;
+    if (CT != kE4M3 || !same) {
       uint32_t carry = 0;
 #pragma unroll
       for (int c = 0; c < VC; ++c)
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
-          for (int i = 0; i < VE / 2; ++i) carry |= (vr[c][t][i] & 0x7fff7fffu) + kOne;
-      odd = __ballot(carry & 0x80008000u) != 0;
+          for (int i = 0; i < VE * EB / 4; ++i) carry |= (vr[c][t][i] & ~kSigns) + kOne;
+      odd = __ballot(carry & kSigns) != 0;
+    }
+    if (CHUNK && odd && !same) {
+      // Some rows do not see it, and 0 * NaN must not reach them: such values
+      // are left out of the product and added to the rows that do.
+#pragma unroll
+      for (int c = 0; c < VC; ++c)
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int i = 0; i < VE * EB / 4; ++i) {
+            const uint32_t w = vr[c][t][i];
+            const uint32_t ones = (((w & ~kSigns) + kOne) & kSigns) >> (8 * EB - 1);
+            vr[c][t][i] = w & ~(ones * (EB == 1 ? 0xffu : 0xffffu));
+          }
+      odd = false;
+#pragma unroll 1
+      for (int k = 0; k < kTile; ++k) {
+        const uint32_t page0 = table[div_by(token_of(min(u0 + k, end - 1)), a.kv.page)];
+        if (!((here >> k) & 1)) continue;
+        const uint32_t j = token_of(u0 + k), slot = j - div_by(j, a.kv.page) * a.kv.page.d;
+        const uint8_t* row = vb + page0 * a.kv.v_page + slot * a.kv.v_tok;
+        const bool in = (sees >> k) & 1;
+#pragma unroll
+        for (int c = 0; c < VC; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int d0 = (c * 16 + lg * 4 + i) * VE;
+            u32x4 w = load_words<VE * EB>(row + (d0 < a.dim ? d0 : 0) * EB);
+            if constexpr (EB == 1) {
+              const u32x2 x = widen4<MT>(w.x), y = widen4<MT>(w.y);
+              w = u32x4{x.x, x.y, y.x, y.y};
+            }
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+              const f32x2 pair = unpack2<MT>(w[e / 2]);
+              const float x = e % 2 ? pair.y : pair.x;
+              o[c][e][i] += in && !(fabsf(x) < INFINITY) ? x : 0.f;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+      }
     }
     if (!odd) {
 #pragma unroll
@@ -539,7 +632,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(DP)) void attn_decode_kerne
     x *= kPScale;
     if (whole) {
       if (d < a.dim)
-        store_from_f32(a.out + seq * a.out_row + (head0 + r) * a.out_head, IO, d,
+        store_from_f32(a.out + row_at(r, a.out_row, a.out_head), IO, d,
                        sum == 0.f ? 0.f : x / sum * a.v_scale);
     } else {
       __hip_atomic_store(mine + i, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -635,7 +728,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(DP)) void attn_decode_kerne
         if (team == 0 && q < quads && d < a.dim) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            store_from_f32(a.out + seq * a.out_row + (head0 + r) * a.out_head, IO, d + i, x[i]);
+            store_from_f32(a.out + row_at(r, a.out_row, a.out_head), IO, d + i, x[i]);
         }
       }
     }
@@ -678,12 +771,12 @@ Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t
 
 constexpr size_t kCounterBytes = static_cast<size_t>(kMaxGroups) * kCounterStride * 4;
 
-template <int CT, int IO, int DP, bool FULL>
+template <int CT, int IO, int DP, bool FULL, bool CHUNK>
 hipError_t launch(const DecodeArgs& a, const Plan& p, hipStream_t stream) {
-  const int heads = std::min(kHeadTile, a.group);
+  const int heads = CHUNK ? kHeadTile : std::min(kHeadTile, a.group);
   size_t lds = static_cast<size_t>(kWaves) * heads * (DP + 4 + 2) * 4;
-  lds = std::max(lds, (static_cast<size_t>(heads) * (p.ranges + 1) + kThreads * 4 + 4) * 4);
-  auto kernel = attn_decode_kernel<CT, IO, DP, FULL>;
+  if (!CHUNK) lds = std::max(lds, (static_cast<size_t>(heads) * (p.ranges + 1) + kThreads * 4 + 4) * 4);
+  auto kernel = attn_decode_kernel<CT, IO, DP, FULL, CHUNK>;
   if (lds > 48 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -694,28 +787,28 @@ hipError_t launch(const DecodeArgs& a, const Plan& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int CT, int IO>
+template <int CT, int IO, bool CHUNK>
 hipError_t launch_dim(const DecodeArgs& a, const Plan& p, hipStream_t stream) {
   switch (a.dim) {
-    case 64: return launch<CT, IO, 64, true>(a, p, stream);
-    case 128: return launch<CT, IO, 128, true>(a, p, stream);
-    case 192: return launch<CT, IO, 192, true>(a, p, stream);
-    case 256: return launch<CT, IO, 256, true>(a, p, stream);
+    case 64: return launch<CT, IO, 64, true, CHUNK>(a, p, stream);
+    case 128: return launch<CT, IO, 128, true, CHUNK>(a, p, stream);
+    case 192: return launch<CT, IO, 192, true, CHUNK>(a, p, stream);
+    case 256: return launch<CT, IO, 256, true, CHUNK>(a, p, stream);
   }
   switch (dim_pad(a.dim)) {
-    case 64: return launch<CT, IO, 64, false>(a, p, stream);
-    case 128: return launch<CT, IO, 128, false>(a, p, stream);
-    case 192: return launch<CT, IO, 192, false>(a, p, stream);
-    default: return launch<CT, IO, 256, false>(a, p, stream);
+    case 64: return launch<CT, IO, 64, false, CHUNK>(a, p, stream);
+    case 128: return launch<CT, IO, 128, false, CHUNK>(a, p, stream);
+    case 192: return launch<CT, IO, 192, false, CHUNK>(a, p, stream);
+    default: return launch<CT, IO, 256, false, CHUNK>(a, p, stream);
   }
 }
 
 template <int CT>
 hipError_t launch_io(int io, const DecodeArgs& a, const Plan& p, hipStream_t stream) {
   switch (io) {
-    case kF32: return launch_dim<CT, kF32>(a, p, stream);
-    case kBF16: return launch_dim<CT, kBF16>(a, p, stream);
-    default: return launch_dim<CT, kF16>(a, p, stream);
+    case kF32: return launch_dim<CT, kF32, false>(a, p, stream);
+    case kBF16: return launch_dim<CT, kBF16, false>(a, p, stream);
+    default: return launch_dim<CT, kF16, false>(a, p, stream);
   }
 }
 
@@ -729,13 +822,13 @@ size_t attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv& kv,
                              (dim_pad(kv.dim) + 4) * 4;
 }
 
-hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t seqs, int64_t heads,
-                              const xq_kv& kv, const TableView& tables, const int32_t* lens,
-                              float scale, int64_t window, int64_t sinks, int64_t max_len, void* ws,
-                              hipStream_t stream) {
-  const Plan p = plan(seqs, heads, kv, max_len, window, sinks);
+namespace {
+
+DecodeArgs fill(const RowsView& out, const RowsView& q, int64_t heads, const xq_kv& kv,
+                const TableView& tables, const int32_t* lens, float scale, int64_t window,
+                int64_t sinks) {
   const int eb = elem_bytes(kv.dtype), ib = elem_bytes(q.type);
-  DecodeArgs a;
+  DecodeArgs a = {};
   a.kv = KvView{static_cast<uint8_t*>(kv.k), static_cast<uint8_t*>(kv.v),
                 kv.k_stride[1] * eb, kv.k_stride[2] * eb, kv.k_stride[3] * eb,
                 kv.v_stride[1] * eb, kv.v_stride[2] * eb, kv.v_stride[3] * eb,
@@ -744,8 +837,6 @@ hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t se
   a.out = static_cast<uint8_t*>(out.data);
   a.tables = tables.data;
   a.lens = lens;
-  a.count = static_cast<int32_t*>(ws);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
   a.q_row = q.row * ib;
   a.q_head = q.head * ib;
   a.out_row = out.row * ib;
@@ -759,20 +850,63 @@ hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t se
   a.k_tok16 = static_cast<uint32_t>(a.kv.k_tok / 16);
   a.v_page16 = static_cast<uint32_t>(a.kv.v_page / 16);
   a.v_tok16 = static_cast<uint32_t>(a.kv.v_tok / 16);
-  a.max_len = static_cast<int>(max_len);
+  a.max_len = 1 << 30;
   a.window = static_cast<int>(window);
   a.sinks = static_cast<int>(sinks);
+  a.c = scale * kv.k_scale * kLog2e;
+  a.v_scale = kv.v_scale;
+  return a;
+}
+
+// Row tiles of a sequence's kv heads.
+int64_t chunk_units(int64_t heads, const xq_kv& kv, int64_t max_chunk) {
+  return kv.kv_heads * ((max_chunk * (heads / kv.kv_heads) + kHeadTile - 1) / kHeadTile);
+}
+
+}  // namespace
+
+hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t seqs, int64_t heads,
+                              const xq_kv& kv, const TableView& tables, const int32_t* lens,
+                              float scale, int64_t window, int64_t sinks, int64_t max_len, void* ws,
+                              hipStream_t stream) {
+  const Plan p = plan(seqs, heads, kv, max_len, window, sinks);
+  DecodeArgs a = fill(out, q, heads, kv, tables, lens, scale, window, sinks);
+  a.count = static_cast<int32_t*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
+  a.max_len = static_cast<int>(max_len);
   a.seqs = static_cast<int>(seqs);
   a.shared = p.shared;
   a.ranges = fast_div(static_cast<uint32_t>(p.ranges));
   a.head_tiles = static_cast<int>(p.per_seq / kv.kv_heads);
-  a.c = scale * kv.k_scale * kLog2e;
-  a.v_scale = kv.v_scale;
   switch (kv.dtype) {
     case kBF16: return launch_io<kBF16>(q.type, a, p, stream);
     case kF16: return launch_io<kF16>(q.type, a, p, stream);
     default: return launch_io<kE4M3>(q.type, a, p, stream);
   }
+}
+
+bool chunk_in_rows(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_chunk) {
+  return seqs * chunk_units(heads, kv, max_chunk) <= 512;
+}
+
+hipError_t launch_attn_chunk(const RowsView& out, const RowsView& q, int64_t rows, int64_t seqs,
+                             int64_t heads, const xq_kv& kv, const TableView& tables,
+                             const int32_t* lens, const int32_t* starts, int64_t max_chunk,
+                             float scale, int64_t window, int64_t sinks, hipStream_t stream) {
+  DecodeArgs a = fill(out, q, heads, kv, tables, lens, scale, window, sinks);
+  Plan p;
+  p.per_seq = chunk_units(heads, kv, max_chunk);
+  p.ranges = seqs;
+  p.shared = false;
+  a.head_tiles = static_cast<int>(p.per_seq / kv.kv_heads);
+  a.starts = starts;
+  a.rows = static_cast<int>(rows);
+  a.max_chunk = static_cast<int>(max_chunk);
+  a.group_div = fast_div(static_cast<uint32_t>(a.group));
+  if (kv.dtype == kBF16) return launch_dim<kBF16, kBF16, true>(a, p, stream);
+  if (kv.dtype == kF16) return launch_dim<kF16, kF16, true>(a, p, stream);
+  return q.type == kBF16 ? launch_dim<kE4M3, kBF16, true>(a, p, stream)
+                         : launch_dim<kE4M3, kF16, true>(a, p, stream);
 }
 
 }  // namespace xq

@@ -494,6 +494,9 @@ hipError_t launch_attn_prefill(const RowsView& out, const RowsView& q, int64_t r
                                int64_t heads, const xq_kv& kv, const TableView& tables,
                                const int32_t* lens, const int32_t* starts, int64_t max_chunk,
                                float scale, int64_t window, int64_t sinks, hipStream_t stream) {
+  if (chunk_in_rows(seqs, heads, kv, max_chunk))
+    return launch_attn_chunk(out, q, rows, seqs, heads, kv, tables, lens, starts, max_chunk, scale, window, sinks,
+                             stream);
   const int eb = elem_bytes(kv.dtype);
   PrefillArgs a;
   a.kv = KvView{static_cast<uint8_t*>(kv.k), static_cast<uint8_t*>(kv.v),

@@ -31,6 +31,13 @@ hipError_t launch_attn_prefill(const RowsView& out, const RowsView& q, int64_t r
                                int64_t heads, const xq_kv& kv, const TableView& tables,
                                const int32_t* lens, const int32_t* starts, int64_t max_chunk,
                                float scale, int64_t window, int64_t sinks, hipStream_t stream);
+// Short chunks, whose (token, head) rows fill at most two workgroups of 16 a CU,
+// run on the single-token kernel's form for rows (launch_attn_chunk).
+bool chunk_in_rows(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_chunk);
+hipError_t launch_attn_chunk(const RowsView& out, const RowsView& q, int64_t rows, int64_t seqs,
+                             int64_t heads, const xq_kv& kv, const TableView& tables,
+                             const int32_t* lens, const int32_t* starts, int64_t max_chunk,
+                             float scale, int64_t window, int64_t sinks, hipStream_t stream);
 // kv (with k, v and slots) may be null: then only q is rotated.
 hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k, const RowsView* v,
                        int64_t tokens, int64_t heads, int64_t dim, const xq_kv* kv,
