@@ -25,6 +25,7 @@
 // needs.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv_device.h"
 #include "kv_launch.h"
@@ -188,7 +189,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     const uint64_t all = __ballot(ok);
     if (lane == 0) found[t % 3] = all;
   };
-  u32x4 kr[PER], vr[PER];
+  using Raw = std::conditional_t<EB == 2, u32x4, u32x2>;
+  Raw kr[PER], vr[PER];
   auto load = [&](int t) {
     uint32_t at[2][PER];
 #pragma unroll
@@ -202,16 +204,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
         const int d0 = (tid + i * kThreads) % CH * 8;
         const uint8_t* p = (w ? vb : kb) + static_cast<uint64_t>(at[w][i]) * 16 +
                            (FULL || d0 < a.dim ? d0 : 0) * EB;
-        u32x4& r = w ? vr[i] : kr[i];
-        if constexpr (EB == 2) {
-          r = *reinterpret_cast<const u32x4*>(p);
-        } else {
-          const u32x2 x = *reinterpret_cast<const u32x2*>(p);
-          r = u32x4{x.x, x.y, 0, 0};
-        }
+        (w ? vr[i] : kr[i]) = *reinterpret_cast<const Raw*>(p);
       }
   };
-  auto widen = [&](u32x4 w) {
+  auto widen = [&](Raw w) {
     if constexpr (EB == 2) {
       return w;
     } else {
@@ -409,24 +405,27 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
       // over tiles, and keep in registers that there are none of.)
       int first_dim = 4 * lh;
       asm volatile("" : "+v"(first_dim));
+#pragma unroll 1
       for (int k = 0; k < kTile; ++k) {
-        const int64_t off = static_cast<int64_t>(places[t % 3][1][k]) * 16;
+        if (!((there >> k) & 1)) continue;
+        const uint8_t* row = vb + static_cast<int64_t>(places[t % 3][1][k]) * 16;
         const bool sees = (vis >> k) & 1;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int dim = d * 32 + 8 * (i / 4) + first_dim + i % 4;
-            if (sees && (FULL || dim < a.dim)) {
-              float x;
-              if constexpr (EB == 2) {
-                x = load_as_f32(vb + off, MT, dim);
-              } else {
-                x = unpack2<MT>(widen4<MT>(vb[off + dim]).x).x;
-              }
-              if (!(fabsf(x) < INFINITY)) o[d][i] += x;
+          for (int i = 0; i < 16; i += 4) {
+            const int dim = d * 32 + 8 * (i / 4) + first_dim;
+            const uint8_t* p = row + (FULL || dim < a.dim ? dim : 0) * EB;
+            u32x2 w;
+            if constexpr (EB == 2) w = *reinterpret_cast<const u32x2*>(p);
+            else w = widen4<MT>(*reinterpret_cast<const uint32_t*>(p));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const f32x2 pair = unpack2<MT>(w[e / 2]);
+              const float x = e % 2 ? pair.y : pair.x;
+              o[d][i + e] += sees && !(fabsf(x) < INFINITY) ? x : 0.f;
             }
-            if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few loads under way: registers are short
+            __builtin_amdgcn_sched_barrier(0);  // few loads under way: registers are short
           }
       }
     }
