@@ -100,18 +100,21 @@ __device__ __forceinline__ u32x4 load_words(const uint8_t* p) {
   }
 }
 
-// Workgroups that a CU is given, its SIMDs one wave of each. Twice as many of
-// 128 dims and more, each with half the work, are slower: 131072 tokens x 2
-// 195 against 174 us, 64 windows of 8192 147 against 138; of 64 dims they are
-// faster (115 -> 95 us).
-constexpr int groups_per_cu(int dp) { return dp == 64 ? 2 : 1; }
+// Workgroups that a CU is given at most, its SIMDs one wave of each. Twice as
+// many of 128 dims and more of a 16-bit cache, each with half the work, are
+// slower: 131072 tokens x 2 195 against 174 us. Of 64 dims they are faster (115
+// -> 95 us), and of an 8-bit cache of up to 128, whose widening then overlaps
+// the loads: 64 windows of 8192 150 -> 138 us, 32 sequences of up to 4099 40 ->
+// 33.5. (With pages stored token by token, where a workgroup's rows lie apart,
+// the latter lose: 131072 tokens x 2 89 -> 100 us; those take one.)
+constexpr int groups_per_cu(int ct, int dp) { return dp == 64 || (ct == kE4M3 && dp == 128) ? 2 : 1; }
 
 // CT: the cache's type. IO: q's and out's. DP: dim rounded up to 64, 128, 192
 // or 256; FULL: dim is DP. CHUNK: several new tokens per sequence; a
 // workgroup's 16 columns are then 16 of a sequence's (token, head) rows, which
 // see different tokens.
 template <int CT, int IO, int DP, bool FULL, bool CHUNK>
-__global__ __launch_bounds__(kThreads, groups_per_cu(DP)) void attn_decode_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_kernel(DecodeArgs a) {
   constexpr int MT = CT == kBF16 ? kBF16 : kF16;   // the matrix instruction's type
   constexpr int EB = CT == kE4M3 ? 1 : 2;
   constexpr int IB = IO == kF32 ? 4 : 2;
@@ -763,7 +766,9 @@ Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t
   p.per_seq = kv.kv_heads * ((group + kHeadTile - 1) / kHeadTile);
   const int64_t most = window && window + sinks < max_len ? window + sinks : max_len;
   const int64_t steps = (most + kStep - 1) / kStep;
-  const int64_t room = 256 * groups_per_cu(dim_pad(kv.dim));
+  const int dp = dim_pad(kv.dim);
+  const bool apart = dp == 128 && kv.k_stride[3] != kv.dim && kv.page > 1;
+  const int64_t room = 256 * (apart ? 1 : groups_per_cu(kv.dtype, dp));
   p.shared = steps > 3 && seqs * p.per_seq < 3 * room && p.per_seq <= room && seqs * steps < (1 << 30);
   p.ranges = p.shared ? std::min(room / p.per_seq, seqs * steps) : seqs;
   return p;
