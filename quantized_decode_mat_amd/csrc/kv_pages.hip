@@ -141,6 +141,92 @@ struct TableArgs {
   int32_t* count;
 };
 
+// Forks, first launch, for up to 1024 of up to kFewSlots rows: a thread keeps
+// its fork in registers, claims and fresh pages stay in LDS, so the launch is
+// four trips to memory (8 us; 10 by the lists in memory).
+constexpr int kFewSlots = 4096;
+__global__ __launch_bounds__(kListThreads) void fork_few_kernel(TableArgs a) {
+  const int tid = threadIdx.x;
+  __shared__ int claim[kFewSlots], parent[kListThreads], pages_of[kListThreads], bad[kListThreads];
+  __shared__ int fresh[kListThreads];
+  const int c = tid < a.n ? a.children[tid] : -1, p = tid < a.n ? a.parents[tid] : -1;
+  int ref[kRun];
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) ref[k] = tid * kRun + k < a.pages ? a.refs[tid * kRun + k] : 1;
+  for (int i = tid; i < a.slots; i += kListThreads) claim[i] = a.n;
+  pages_of[tid] = 0;
+  bad[tid] = 0;
+  __syncthreads();
+  if (c >= 0 && c < a.slots) atomicMin(claim + c, tid);
+  __syncthreads();
+  int len = -1;
+  if (c >= 0 && c < a.slots && p >= 0 && p < a.slots && claim[c] == tid) {
+    const int own = a.lens[c], of_parent = a.lens[p];
+    if (own == 0 && (static_cast<int64_t>(of_parent) + a.page - 1) / a.page <= a.width) len = of_parent;
+  }
+  if (len > 0) {
+    parent[tid] = p;
+    pages_of[tid] = static_cast<int>((static_cast<int64_t>(len) + a.page - 1) / a.page);
+  }
+  __syncthreads();
+  // All the parents' pages, entry by entry.
+  const int64_t entries = static_cast<int64_t>(a.n) * a.width;
+#pragma unroll 4
+  for (int64_t k = tid; k < entries; k += kListThreads) {
+    const int f = static_cast<int>(k / a.width), e = static_cast<int>(k - static_cast<int64_t>(f) * a.width);
+    if (e < pages_of[f] &&
+        static_cast<uint32_t>(a.tables[parent[f] * a.stride + e]) >= static_cast<uint32_t>(a.pages))
+      bad[f] = 1;
+  }
+  __syncthreads();
+  if (bad[tid]) len = -1;
+  const int part = len > 0 && len % a.page > 0;
+  int need;
+  const int mine = group_scan(part, &need);
+  // The first `need` free pages, ascending, by number.
+  int found = 0;
+  for (int64_t p0 = 0; p0 < a.pages && found < need; p0 += kListThreads * kRun) {
+    const int64_t q = p0 + tid * kRun;
+    if (p0) {
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) ref[k] = q + k < a.pages ? a.refs[q + k] : 1;
+    }
+    int free = 0, total;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) free += ref[k] == 0;
+    int at = found + group_scan(free, &total);
+#pragma unroll
+    for (int k = 0; k < kRun; ++k)
+      if (ref[k] == 0) {
+        if (at < need) fresh[at] = static_cast<int>(q + k);
+        ++at;
+      }
+    found += total;
+  }
+  __syncthreads();
+  int from = -1, to = -1;
+  if (part) {
+    if (mine < found) {
+      to = fresh[mine];
+      from = a.tables[p * a.stride + len / a.page];
+      a.refs[to] = 1;
+    } else {
+      len = -1;
+    }
+  }
+  if (tid < a.n) {
+    a.len[tid] = len;
+    a.src[tid] = from;
+    a.dst[tid] = to;
+  }
+  int refused;
+  group_scan(tid < a.n && len < 0, &refused);
+  if (tid == 0) {
+    a.status[0] = refused;
+    a.status[1] = max(0, need - found);
+  }
+}
+
 // Forks, first launch: which are sound, and a fresh page for each that needs
 // one.
 __global__ __launch_bounds__(kListThreads) void fork_list_kernel(TableArgs a) {
@@ -265,6 +351,81 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(TableArgs a, PageArgs pa
     return;
   }
   copy_pairs(pa, a.src, a.dst, a.n, blockIdx.x - a.n, gridDim.x - a.n);
+}
+
+// Compaction, first launch, for up to kListThreads * kRun pages: a thread keeps
+// its pages' counts in registers and finds each mover's hole in LDS. Page k *
+// 1024 + t is thread t's, so that every access is a wave's neighbours (with
+// eight pages in a row to a thread the stores took 13 us); a page's number
+// among the holes or movers is that of its wave's 64 pages and a bit count.
+__global__ __launch_bounds__(kListThreads) void compact_few_kernel(TableArgs a) {
+  constexpr int kListWaves = kListThreads / kWave;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  __shared__ int hole_at[kListThreads * kRun / 2];  // no more holes below the live pages than half
+  __shared__ int used_in[kListWaves], counts[kRun * kListWaves];
+  int ref[kRun], used = 0;
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    const int page = k * kListThreads + tid;
+    ref[k] = page < a.pages ? a.refs[page] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) used += __popcll(__ballot(ref[k] > 0));
+  if (lane == 0) used_in[wave] = used;
+  __syncthreads();
+  int live = 0;
+#pragma unroll
+  for (int i = 0; i < kListWaves; ++i) live += used_in[i];
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    const int page = k * kListThreads + tid;
+    const uint64_t holes = __ballot(page < live && ref[k] <= 0), movers = __ballot(page >= live && ref[k] > 0);
+    // At most 4096 of each before any page.
+    if (lane == 0) counts[k * kListWaves + wave] = __popcll(holes) | (__popcll(movers) << 16);
+  }
+  __syncthreads();
+  if (wave == 0) {
+    const int x0 = counts[2 * lane], x1 = counts[2 * lane + 1];
+    int x = x0 + x1;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int u = __shfl_up(x, d, kWave);
+      if (lane >= d) x += u;
+    }
+    if (lane == kWave - 1) *a.count = x >> 16;
+    counts[2 * lane] = x - x0 - x1;
+    counts[2 * lane + 1] = x - x1;
+  }
+  __syncthreads();
+  const uint64_t before = (1ull << lane) - 1;
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    const int page = k * kListThreads + tid;
+    const bool hole = page < live && ref[k] <= 0;
+    const uint64_t holes = __ballot(hole);
+    if (hole) hole_at[(counts[k * kListWaves + wave] & 0xffff) + __popcll(holes & before)] = page;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    const int page = k * kListThreads + tid;
+    const bool mover = page >= live && ref[k] > 0;
+    const uint64_t movers = __ballot(mover);
+    int to = page;
+    if (mover) {
+      const int at = (counts[k * kListWaves + wave] >> 16) + __popcll(movers & before);
+      to = hole_at[at];
+      a.src[at] = page;
+      a.dst[at] = to;
+      a.refs[to] = ref[k];
+      a.refs[page] = 0;
+    }
+    if (page < a.pages) a.map[page] = to;
+  }
+  if (tid == 0) {
+    a.status[0] = 0;
+    a.status[1] = live;
+  }
 }
 
 // Compaction, first launch: the pages that move, where every page goes, and
@@ -434,7 +595,10 @@ hipError_t launch_cache_fork(const xq_kv& kv, int32_t* refs, int32_t* tables, in
   t.parents = parents;
   t.children = children;
   t.n = static_cast<int>(n);
-  fork_list_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
+  if (n <= kListThreads && slots <= kFewSlots)
+    fork_few_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
+  else
+    fork_list_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || n == 0) return e;
   const PageArgs a = page_args(kv);
@@ -446,7 +610,10 @@ hipError_t launch_cache_compact(const xq_kv& kv, int32_t* refs, int32_t* tables,
                                 int64_t width, int64_t stride, int32_t* status, void* ws,
                                 hipStream_t stream) {
   const TableArgs t = table_args(kv, refs, tables, slots, width, stride, status, ws);
-  compact_list_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
+  if (kv.pages <= kListThreads * kRun)
+    compact_few_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
+  else
+    compact_list_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const PageArgs a = page_args(kv);
