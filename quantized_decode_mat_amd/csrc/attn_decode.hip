@@ -28,6 +28,10 @@
 // twice the registers, or K turned round in LDS after whole-row loads, were
 // both slower.)
 //
+// Measured: 2 sequences of up to 131072, 32 heads of 128 dims on 8 kv heads, bf16
+// cache: 163-171 us, 6.0-6.3 TB/s (a streaming read: 7.3); 64 windows of 8192 of
+// 8 bits 132-138 us; one sequence of 517 11.2 us, of which the join is 3.6.
+//
 // Precision: q and the weights p enter the 16-bit matrix instructions as sums
 // of pieces (each the rounded remainder of the one before). For a 16-bit
 // output: q exactly, p in two pieces (2^-16 or better). For an f32 output: as
@@ -890,6 +894,12 @@ hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t se
   }
 }
 
+// Tiles of 16 rows, each walked by a workgroup's four waves in steps of 128
+// tokens, against tiles of 128 rows in steps of 64: as long as all of the
+// former are on the card at once they are the shorter walk. 11 new tokens on
+// 1530 (8 bits) 25 against 73 us, 364 on 624 with 8 heads 18 against 26, 90 on
+// 1976 of 192 dims 26 against 39; but 8 on 92 of 192 dims 16.5 against 12. The
+// batch of 7 chunks of up to 300 on 4 kv heads of 4 has 2100 and stays there.
 bool chunk_in_rows(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_chunk) {
   return seqs * chunk_units(heads, kv, max_chunk) <= 512;
 }

