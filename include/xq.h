@@ -417,8 +417,8 @@ size_t xq_attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv *
  * j > p - window, or j < sinks). The sum is xq_attn_decode's. A row that sees
  * nothing (a position below 0, pages that are missing) gives zeros. A token
  * that a row does not see has no influence on it, whatever its bytes are.
- * The weights p are rounded to the cache's type (io for an 8-bit cache)
- * before their product with v; sums and maxima are f32.
+ * The weights p enter their product with v rounded to 16 bits (io's, or better
+ * where the rows are few); sums and maxima are f32.
  *
  *  out, q   device [rows][heads][dim] of type io, XQ_BF16 or XQ_F16; the
  *           cache's type is io or XQ_E4M3. Strides and alignment as in
