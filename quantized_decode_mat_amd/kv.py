@@ -14,9 +14,37 @@ import ctypes
 
 import torch
 
-from . import XQError, _check, _workspace, lib  # noqa: F401
+from . import _check as _raise
+from . import lib as _load
 
 XQ_F32, XQ_BF16, XQ_F16, XQ_E4M3 = range(4)
+_L = None
+
+
+def lib():
+    """The loaded library; these calls are a few microseconds, so it is kept at hand."""
+    global _L
+    if _L is None:
+        _L = _load()
+    return _L
+
+
+def _check(status: int, func: str):
+    if status:
+        _raise(status, func)
+
+
+def _workspace(ws, index: int):
+    """(pointer, bytes) of a workspace tensor; the library holds them against its need."""
+    if ws is None:
+        return None, 0
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on device %d" % index)
+    return ws.data_ptr(), ws.nbytes
+
+
 _ROW = {torch.float32: XQ_F32, torch.bfloat16: XQ_BF16, torch.float16: XQ_F16}
 _CACHE = {torch.bfloat16: XQ_BF16, torch.float16: XQ_F16, torch.float8_e4m3fn: XQ_E4M3}
 
@@ -120,8 +148,8 @@ def _rows(t, what: str, index: int):
     st = t.stride()
     if len(st) != 3 or st[2] != 1:
         raise ValueError("%s: expected [rows, heads, dim] with contiguous dims" % what)
-    rows, heads, _ = t.shape
-    return t.data_ptr(), kind, st[0] if rows != 1 else 0, st[1] if heads != 1 else 0
+    shape = t.shape
+    return t.data_ptr(), kind, st[0] if shape[0] != 1 else 0, st[1] if shape[1] != 1 else 0
 
 
 def _ints(t, what: str, index: int, n: int, dtype=torch.int32):
@@ -136,10 +164,11 @@ def _table(t, what: str, index: int, rows: int):
     """(pointer, width, stride) of a table of pages."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s: expected a torch.Tensor" % what)
-    if (t.get_device() != index or t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != rows
-            or (t.shape[1] > 1 and t.stride(1) != 1)):
+    shape, st = t.shape, t.stride()
+    if (t.get_device() != index or t.dtype != torch.int32 or len(shape) != 2 or shape[0] != rows
+            or (shape[1] > 1 and st[1] != 1)):
         raise ValueError("%s: expected int32 [%d, width] on device %d" % (what, rows, index))
-    return t.data_ptr(), t.shape[1], t.stride(0) if rows != 1 else t.shape[1]
+    return t.data_ptr(), shape[1], st[0] if rows != 1 else shape[1]
 
 
 def xq_attn_decode_workspace_bytes(seqs: int, heads: int, kv: xq_kv_cache, max_len: int,
@@ -168,7 +197,7 @@ def xq_attn_decode(out, q, kv: xq_kv_cache, tables, lens, scale: float, window: 
     tp, width, t_stride = _table(tables, "tables", index, seqs)
     if max_len is None:
         max_len = width * kv.page
-    wp, wb = (None, 0) if workspace is None else _workspace(workspace, 0)
+    wp, wb = _workspace(workspace, index)
     _check(lib().xq_attn_decode(op, qp, kind, seqs, heads, out_row, out_head, q_row, q_head, kv._ref, tp,
                                 width, t_stride, _ints(lens, "lens", index, seqs), scale, window, sinks,
                                 max_len, wp, wb, _raw_stream(stream, index)),
@@ -272,7 +301,7 @@ def xq_cache_fork(kv: xq_kv_cache, refs, tables, lens, parents, children, status
     [refused forks, free pages lacking]."""
     index, slots, n = kv.index, lens.numel(), children.numel()
     tp, width, t_stride = _table(tables, "tables", index, slots)
-    wp, wb = (None, 0) if workspace is None else _workspace(workspace, 0)
+    wp, wb = _workspace(workspace, index)
     _check(lib().xq_cache_fork(kv._ref, _ints(refs, "refs", index, kv.pages), tp, slots, width, t_stride,
                                _ints(lens, "lens", index, slots), _ints(parents, "parents", index, n),
                                _ints(children, "children", index, n), n, _ints(status, "status", index, 2),
@@ -284,7 +313,7 @@ def xq_cache_compact(kv: xq_kv_cache, refs, tables, status, workspace=None, stre
     """The live pages move together at the front; status is [0, live pages]."""
     index, slots = kv.index, tables.shape[0]
     tp, width, t_stride = _table(tables, "tables", index, slots)
-    wp, wb = (None, 0) if workspace is None else _workspace(workspace, 0)
+    wp, wb = _workspace(workspace, index)
     _check(lib().xq_cache_compact(kv._ref, _ints(refs, "refs", index, kv.pages), tp, slots, width, t_stride,
                                   _ints(status, "status", index, 2), wp, wb, _raw_stream(stream, index)),
            "xq_cache_compact")
