@@ -40,6 +40,7 @@
 #include <algorithm>
 
 #include "kv_device.h"
+#include "kv_lanes.h"
 #include "kv_launch.h"
 
 namespace xq {
@@ -129,9 +130,10 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   // 16 bytes of K give KL instructions their operand: an 8-bit row's are 16
   // dims, two instructions' worth.
   constexpr int KL = CT == kE4M3 ? 2 : 1;
-  constexpr int KN = QS / KL;                      // K loads of a lane per token
-  constexpr int VE = DP == 64 ? 4 : 8;             // dims of a lane's V load
-  constexpr int VC = (DP + 16 * VE - 1) / (16 * VE);
+  constexpr int KN = decode_k_loads(DP, EB);       // K loads of a lane per token
+  static_assert(KN * KL == QS);
+  constexpr int VE = decode_v_dims(DP);            // dims of a lane's V load
+  constexpr int VC = decode_v_loads(DP);
   constexpr int OS = DP + 4;                       // floats of a joined row in LDS
   extern __shared__ float lds[];
   __shared__ __attribute__((aligned(16))) uint32_t places[kWaves][2][kTile];
@@ -282,10 +284,8 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     for (int t = 0; t < 2; ++t) {
       const uint8_t* p = kb + static_cast<uint64_t>(at[t]) * 16;
 #pragma unroll
-      for (int s = 0; s < KN; ++s) {
-        const int d0 = s * 32 * KL + lg * 8 * KL;
-        kr[t][s] = *reinterpret_cast<const u32x4*>(p + (FULL || d0 < a.dim ? d0 : 0) * EB);
-      }
+      for (int s = 0; s < KN; ++s)
+        kr[t][s] = *reinterpret_cast<const u32x4*>(p + decode_k_dim<DP, FULL>(s, lg, EB, a.dim) * EB);
     }
   };
   auto load_v = [&]() {
@@ -297,11 +297,8 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     for (int t = 0; t < 8; ++t) {
       const uint8_t* p = vb + static_cast<uint64_t>(at[t / 4][t % 4]) * 16;
 #pragma unroll
-      for (int c = 0; c < VC; ++c) {
-        // Dims past the end are read from the start; nothing uses them.
-        const int d0 = (c * 16 + l16) * VE;
-        vr[c][t] = load_words<VE * EB>(p + (FULL || d0 < a.dim ? d0 : 0) * EB);
-      }
+      for (int c = 0; c < VC; ++c)  // (what stands for dims past the end nothing uses)
+        vr[c][t] = load_words<VE * EB>(p + decode_v_dim<DP, FULL>(c, l16, a.dim) * EB);
     }
   };
   auto widen_v = [&](const u32x4(&r)[8], u32x4(&w)[8]) {
@@ -536,8 +533,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
         for (int c = 0; c < VC; ++c)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int d0 = (c * 16 + lg * 4 + i) * VE;
-            u32x4 w = load_words<VE * EB>(row + (d0 < a.dim ? d0 : 0) * EB);
+            u32x4 w = load_words<VE * EB>(row + decode_v_dim<DP, FULL>(c, lg * 4 + i, a.dim) * EB);
             if constexpr (EB == 1) {
               const u32x2 x = widen4<MT>(w.x), y = widen4<MT>(w.y);
               w = u32x4{x.x, x.y, y.x, y.y};
@@ -751,8 +747,6 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   }
 }
 
-int dim_pad(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256; }
-
 struct Plan {
   int64_t per_seq, ranges;  // units of a sequence; parts of all sequences' steps
   bool shared;
@@ -770,7 +764,7 @@ Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t
   p.per_seq = kv.kv_heads * ((group + kHeadTile - 1) / kHeadTile);
   const int64_t most = window && window + sinks < max_len ? window + sinks : max_len;
   const int64_t steps = (most + kStep - 1) / kStep;
-  const int dp = dim_pad(kv.dim);
+  const int dp = decode_dim_pad(static_cast<int>(kv.dim));
   const bool apart = dp == 128 && kv.k_stride[3] != kv.dim && kv.page > 1;
   const int64_t room = 256 * (apart ? 1 : groups_per_cu(kv.dtype, dp));
   p.shared = steps > 3 && seqs * p.per_seq < 3 * room && p.per_seq <= room && seqs * steps < (1 << 30);
@@ -804,7 +798,7 @@ hipError_t launch_dim(const DecodeArgs& a, const Plan& p, hipStream_t stream) {
     case 192: return launch<CT, IO, 192, true, CHUNK>(a, p, stream);
     case 256: return launch<CT, IO, 256, true, CHUNK>(a, p, stream);
   }
-  switch (dim_pad(a.dim)) {
+  switch (decode_dim_pad(a.dim)) {
     case 64: return launch<CT, IO, 64, false, CHUNK>(a, p, stream);
     case 128: return launch<CT, IO, 128, false, CHUNK>(a, p, stream);
     case 192: return launch<CT, IO, 192, false, CHUNK>(a, p, stream);
@@ -828,7 +822,7 @@ size_t attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv& kv,
   const Plan p = plan(seqs, heads, kv, max_len, window, sinks);
   if (!p.shared) return 0;
   return kCounterBytes + static_cast<size_t>(p.per_seq * p.ranges) * 2 * std::min<int64_t>(kHeadTile, heads / kv.kv_heads) *
-                             (dim_pad(kv.dim) + 4) * 4;
+                             (decode_dim_pad(static_cast<int>(kv.dim)) + 4) * 4;
 }
 
 namespace {
