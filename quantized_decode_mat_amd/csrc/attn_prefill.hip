@@ -59,6 +59,7 @@ struct PrefillArgs {
   int rows, seqs, kv_heads, dim, max_chunk, window, sinks, tiles;
   uint32_t k_page16, k_tok16, v_page16, v_tok16;  // in 16-byte units
   int flip;       // q's sign is turned, for a negative scale
+  int zero;       // q counts as 0, for a scale of 0 (c is 1 then: -infinity hides a score only if c > 0)
   float c;        // |scale| * k_scale * log2(e)
   float v_scale;
 };
@@ -171,7 +172,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     for (int s = 0; s < DP / 16; ++s) {
       const int d0 = s * 16 + lh * 8;
       qf[s] = u32x4{0, 0, 0, 0};
-      if (mine && d0 < a.dim) qf[s] = *reinterpret_cast<const u32x4*>(qr + d0 * 2);
+      if (mine && d0 < a.dim && !a.zero) qf[s] = *reinterpret_cast<const u32x4*>(qr + d0 * 2);
       if (a.flip) qf[s] ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
     }
   }
@@ -536,6 +537,8 @@ hipError_t launch_attn_prefill(const RowsView& out, const RowsView& q, int64_t r
   a.v_tok16 = static_cast<uint32_t>(a.kv.v_tok / 16);
   a.flip = scale < 0.f;
   a.c = std::fabs(scale) * kv.k_scale * kLog2e;
+  a.zero = a.c == 0.f;
+  if (a.zero) a.c = 1.f;
   a.v_scale = kv.v_scale;
   const uint32_t blocks = static_cast<uint32_t>(attn_prefill_blocks(seqs, heads, kv, max_chunk));
   if (q.type == kBF16)

@@ -37,3 +37,17 @@ def test_what_lies_beside_a_row_has_no_influence(cache, io, dim):
         check_prefill(t, lens, [1, 1, 1], [0, 1, 2, 3], 0, 0, "single rows")
         results.append(t["out"].clone())
     assert torch.equal(results[0], results[2]) and torch.equal(results[1], results[3])
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("cache,io,scale,k_scale", [("bf16", "bf16", 0.0, 1.0), ("f16", "f16", 0.0, 1.0),
+                                                   ("e4m3", "bf16", 0.0, 0.75), ("e4m3", "f16", 1e-30, 1e-20)])
+def test_scale_of_zero(cache, io, scale, k_scale, many):
+    """Every visible token weighs the same."""
+    n = copies([64, 129], 4, 2) if many else 1
+    lens, chunks = [300, 129] * n, [64, 129] * n
+    s = setup(lens, 4, 2, 80, 16, cache, io, "hnd", rows=193 * n)
+    s["scale"], s["scales"] = scale, (k_scale, s["scales"][1])
+    s["kv"] = xq.xq_kv_cache(s["k"], s["v"], *s["scales"])
+    starts = prefill(s, chunks, 50, 2)
+    check_prefill(s, lens, chunks, starts, 50, 2, "scale of zero")
