@@ -391,6 +391,7 @@ typedef struct {
  *           pages per row; lens device int32[seqs].
  *  heads a multiple of kv_heads, heads / kv_heads <= 256, seqs * kv_heads <= 2^20;
  *  k, and v, of one layer within 64 GiB.
+ *  scale finite, and scale * k_scale * log2(e) too.
  *  window in 0..2^30 (0: none), sinks in 0..2^30 (read only with a window).
  *  max_len in 1..2^30: no length is above it (longer ones are clamped); the split of
  *  the work is planned for it, the result of a given plan is the same from

@@ -77,6 +77,9 @@ xq_status check_attention(int64_t heads, const xq_kv* kv, float scale, int64_t w
   if (heads / kv->kv_heads > 256)
     return fail(XQ_E_SHAPE, "heads/kv_heads=%lld above 256", (long long)(heads / kv->kv_heads));
   if (!std::isfinite(scale)) return fail(XQ_E_SHAPE, "scale=%g not finite", scale);
+  // The kernels' exponents are of 2.
+  if (!std::isfinite(scale * kv->k_scale * 1.44269504f))
+    return fail(XQ_E_SHAPE, "scale=%g times k_scale=%g above f32's range", scale, kv->k_scale);
   for (const int64_t* st : {kv->k_stride, kv->v_stride}) {
     // The kernels find a token by its place within a head, in 16-byte units.
     const double last = static_cast<double>(kv->pages - 1) * static_cast<double>(st[1]) +
