@@ -270,12 +270,26 @@ hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k
   const int64_t blocks = (tokens + a.per_block - 1) / a.per_block;
   a.head_blocks = static_cast<int>(std::clamp<int64_t>(1024 / blocks, 1, (items + kThreads - 1) / kThreads));
   const size_t lds = static_cast<size_t>(a.per_block) * a.half * 2 * sizeof(float);
-  const dim3 grid(static_cast<uint32_t>(blocks * a.head_blocks));
-  if (vec)
-    rope_kernel<true><<<grid, dim3(kThreads), lds, stream>>>(a);
-  else
-    rope_kernel<false><<<grid, dim3(kThreads), lds, stream>>>(a);
-  return hipGetLastError();
+  // A launch's threads are counted in 32 bits, and more wrap round without an
+  // error: so many workgroups (of 2^24 - 1) take the tokens in several launches.
+  const int64_t most = int64_t{1} << 23;
+  for (int64_t left = blocks; left > 0; left -= most) {
+    const int64_t now = std::min(left, most), done = now * a.per_block;
+    a.tokens = static_cast<int>(std::min(done, tokens));
+    const dim3 grid(static_cast<uint32_t>(now * a.head_blocks));
+    if (vec)
+      rope_kernel<true><<<grid, dim3(kThreads), lds, stream>>>(a);
+    else
+      rope_kernel<false><<<grid, dim3(kThreads), lds, stream>>>(a);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    tokens -= done;
+    for (int i = 0; i < 3; ++i)
+      if (a.src[i]) a.src[i] += done * a.row[i];
+    a.out += done * a.out_row;
+    a.pos += done;
+    if (a.slots) a.slots += done;
+  }
+  return hipSuccess;
 }
 
 }  // namespace xq

@@ -7,6 +7,7 @@ import kv_reference as ref
 import quantized_decode_mat_amd as xq
 from test_gpu_kv_attention import _device, check_decode, check_prefill, decode, prefill, setup  # noqa: F401
 from test_gpu_kv_prefill_large import copies
+from test_gpu_kv_rope_pages import check_rope, freqs
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -51,3 +52,41 @@ def test_scale_of_zero(cache, io, scale, k_scale, many):
     s["kv"] = xq.xq_kv_cache(s["k"], s["v"], *s["scales"])
     starts = prefill(s, chunks, 50, 2)
     check_prefill(s, lens, chunks, starts, 50, 2, "scale of zero")
+
+
+def test_rope_of_more_tokens_than_a_launch_has_threads():
+    tokens, plan = (1 << 26) + 5, xq.xq_rope_plan(freqs(8), [4])
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(1 << 20, 1, 8, device=DEV, generator=g).to(torch.bfloat16).repeat(65, 1, 1)[:tokens]
+    pos = torch.arange(tokens, dtype=torch.int32, device=DEV)
+    out = torch.zeros_like(x)
+    xq.xq_rope(out, x, pos, plan)
+    torch.cuda.synchronize()
+    for at in (0, 1 << 22, 1 << 24, 1 << 25, tokens - 40):
+        part = slice(at, at + 40)
+        check_rope(out[part], x[part], pos[None, part], plan, [4], False, False, "bf16")
+    assert (out.view(-1, 8) != 0).any(-1).all()
+
+
+def test_append_of_more_tokens_than_a_launch_has_workgroups():
+    """One row of q, k and v for all tokens; each has its own position and slot."""
+    tokens, heads, dim, page = (1 << 24) + 5, 4, 256, 64
+    plan = xq.xq_rope_plan(freqs(32), [16])
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randn(1, heads + 2, dim, device=DEV, generator=g).expand(tokens, -1, -1)
+    pages = -(-tokens // page)
+    k, v = (torch.zeros(pages, 1, page, dim, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2))
+    pos = torch.arange(tokens, dtype=torch.int32, device=DEV)
+    slots = torch.arange(tokens - 1, -1, -1, device=DEV)
+    out = torch.zeros(tokens, heads, dim, dtype=torch.bfloat16, device=DEV)
+    xq.xq_rope_append(out, xq.xq_kv_cache(k, v, 0.05, 0.04), x[:, :heads], x[:, heads:heads + 1], x[:, heads + 1:], pos,
+                      plan, slots)
+    torch.cuda.synchronize()
+    for at in (0, (1 << 23) - 20, 1 << 23, tokens - 40):
+        part = slice(at, at + 40)
+        check_rope(out[part], x[part, :heads], pos[None, part], plan, [16], False, False, "bf16")
+        page_of, place = slots[part] // page, slots[part] % page
+        check_rope(k.view(torch.uint8)[page_of, :, place].view(k.dtype), x[part, heads:heads + 1], pos[None, part], plan,
+                   [16], False, False, "e4m3", 0.05)
+        want = (x[part, heads + 1:] / 0.04).to(k.dtype)
+        assert torch.equal(v.view(torch.uint8)[page_of, :, place], want.view(torch.uint8))
