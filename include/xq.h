@@ -389,7 +389,8 @@ typedef struct {
  *           bases 16-byte aligned.
  *  tables   device int32, row b at tables + b * table_stride, table_width
  *           pages per row; lens device int32[seqs].
- *  heads a multiple of kv_heads, heads / kv_heads <= 256, seqs * kv_heads <= 2^20;
+ *  heads a multiple of kv_heads, heads / kv_heads <= 256, seqs * kv_heads <= 2^20,
+ *  seqs * kv_heads * ceil(heads / kv_heads / 16) < 2^24;
  *  k, and v, of one layer within 64 GiB.
  *  scale finite, and scale * k_scale * log2(e) too.
  *  window in 0..2^30 (0: none), sinks in 0..2^30 (read only with a window).
@@ -426,7 +427,9 @@ size_t xq_attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv *
  *           xq_attn_decode. Rows of out that no sequence names stay as they are.
  *  starts   device int32[seqs + 1], ascending from >= 0 to <= rows; a
  *           sequence's part outside 0..rows or beyond max_chunk is left out.
- *  max_chunk in 1..rows: the longest chunk; rows * heads <= 2^31 - 1, seqs <= 2^16.
+ *  max_chunk in 1..rows: the longest chunk; rows * heads <= 2^31 - 1, seqs <= 2^16,
+ *  seqs * kv_heads * ceil(max_chunk * heads / kv_heads / 128) < 2^24. The cache,
+ *  heads, scale, window and sinks as xq_attn_decode.
  * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
  */
 xq_status xq_attn_prefill(void *out, const void *q, int32_t io, int64_t rows, int64_t seqs,

@@ -747,6 +747,11 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   }
 }
 
+// Units of a sequence: a kv head and 16 of its heads each.
+int64_t units_of(int64_t heads, const xq_kv& kv) {
+  return kv.kv_heads * ((heads / kv.kv_heads + kHeadTile - 1) / kHeadTile);
+}
+
 struct Plan {
   int64_t per_seq, ranges;  // units of a sequence; parts of all sequences' steps
   bool shared;
@@ -760,8 +765,7 @@ struct Plan {
 Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t window,
           int64_t sinks) {
   Plan p;
-  const int64_t group = heads / kv.kv_heads;
-  p.per_seq = kv.kv_heads * ((group + kHeadTile - 1) / kHeadTile);
+  p.per_seq = units_of(heads, kv);
   const int64_t most = window && window + sinks < max_len ? window + sinks : max_len;
   const int64_t steps = (most + kStep - 1) / kStep;
   const int dp = decode_dim_pad(static_cast<int>(kv.dim));
@@ -816,6 +820,8 @@ hipError_t launch_io(int io, const DecodeArgs& a, const Plan& p, hipStream_t str
 }
 
 }  // namespace
+
+int64_t attn_decode_units(int64_t seqs, int64_t heads, const xq_kv& kv) { return seqs * units_of(heads, kv); }
 
 size_t attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len,
                                    int64_t window, int64_t sinks) {

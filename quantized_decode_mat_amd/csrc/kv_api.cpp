@@ -12,6 +12,9 @@ namespace {
 
 constexpr int64_t kMaxInt = 2147483647LL;
 constexpr int64_t kMaxLen = 1LL << 30;
+// Workgroups of 256 threads: a launch counts its threads in 32 bits, and more
+// wrap round without an error.
+constexpr int64_t kMaxBlocks = (1LL << 24) - 1;
 
 int type_bytes(int32_t t) { return t == XQ_F32 ? 4 : t == XQ_E4M3 ? 1 : 2; }
 bool row_type(int32_t t) { return t == XQ_F32 || t == XQ_BF16 || t == XQ_F16; }
@@ -108,6 +111,8 @@ xq_status check_decode(int64_t seqs, int64_t heads, const xq_kv* kv, float scale
                 (long long)kv->kv_heads);
   if (max_len < 1 || max_len > kMaxLen)
     return fail(XQ_E_SHAPE, "max_len=%lld outside 1..2^30", (long long)max_len);
+  if (xq::attn_decode_units(seqs, heads, *kv) > kMaxBlocks)
+    return fail(XQ_E_SHAPE, "seqs and heads give too many workgroups for one launch");
   return XQ_OK;
 }
 
@@ -181,7 +186,7 @@ xq_status xq_attn_prefill(void *out, const void *q, int32_t io, int64_t rows, in
   if (max_chunk < 1 || max_chunk > rows)
     return fail(XQ_E_SHAPE, "max_chunk=%lld outside 1..rows=%lld", (long long)max_chunk,
                 (long long)rows);
-  if (xq::attn_prefill_blocks(seqs, heads, *kv, max_chunk) > (1 << 24))
+  if (xq::attn_prefill_blocks(seqs, heads, *kv, max_chunk) > kMaxBlocks)
     return fail(XQ_E_SHAPE, "seqs, heads and max_chunk give too many workgroups for one launch");
   if (xq_status s = check_strides(out_row, out_head, "out")) return s;
   if (xq_status s = check_strides(q_row, q_head, "q")) return s;

@@ -20,6 +20,8 @@ struct TableView {
   int64_t width, stride;
 };
 
+// (Sequence, kv head, 16 of its heads) units, each at most a workgroup.
+int64_t attn_decode_units(int64_t seqs, int64_t heads, const xq_kv& kv);
 size_t attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len,
                                    int64_t window, int64_t sinks);
 hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t seqs, int64_t heads,

@@ -11,3 +11,14 @@ from test_kv_abi import SHAPE, call
 def test_scales_whose_product_overflows(name, scale, k_scale):
     s, err = call(name, dict(scale=scale, kv_k_scale=k_scale))
     assert s == SHAPE and "above f32's range" in err, err
+
+
+@pytest.mark.parametrize("name,change", [
+    # 2^20 units of 256 heads, 16 at a time
+    ("xq_attn_decode", dict(seqs=1 << 20, heads=256, kv_kv_heads=1)),
+    # 2^16 sequences of 2^8 tiles of 128 rows
+    ("xq_attn_prefill", dict(seqs=1 << 16, heads=1, kv_kv_heads=1, rows=1 << 15, max_chunk=1 << 15)),
+])
+def test_more_workgroups_than_a_launch_counts(name, change):
+    s, err = call(name, change)
+    assert s == SHAPE and "too many workgroups" in err, err
