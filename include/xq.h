@@ -125,13 +125,14 @@ xq_status xq_gemv_q4k(float *y, const void *w, const void *xq, int64_t N, int64_
  *  w, xq, K as xq_gemv_q4k.
  *  N a multiple of 256, 256 <= N <= 2^22.
  *  workspace  the block counters: xq_gemv_q4k_q8k_workspace_bytes(N) bytes
- *      (one 128-byte line per q8_K block of y), zeroed before first use; the
- *      last arrival at a counter resets it.
+ *      (one 128-byte line per q8_K block of y, at most 768 lines, which more
+ *      blocks share), zeroed before first use; the last arrival at a counter
+ *      resets it.
  * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
  */
 xq_status xq_gemv_q4k_q8k(float *y, void *yq, const void *w, const void *xq, int64_t N, int64_t K,
                           void *workspace, size_t workspace_bytes, void *stream);
-size_t xq_gemv_q4k_q8k_workspace_bytes(int64_t N);  /* N/256 * 128; 0 if N is invalid */
+size_t xq_gemv_q4k_q8k_workspace_bytes(int64_t N);  /* min(N/256, 768) * 128; 0 if N is invalid */
 
 /*
  * IQ4_NL x q8_K decode mat-vec, batch 1 ("25 — Writing XPU Kernels", section

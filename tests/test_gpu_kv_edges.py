@@ -5,6 +5,7 @@ import torch
 
 import kv_reference as ref
 import quantized_decode_mat_amd as xq
+import workloads as wl
 from test_gpu_kv_attention import _device, check_decode, check_prefill, decode, prefill, setup  # noqa: F401
 from test_gpu_kv_prefill_large import copies
 from test_gpu_kv_rope_pages import check_rope, freqs
@@ -90,3 +91,33 @@ def test_append_of_more_tokens_than_a_launch_has_workgroups():
                    [16], False, False, "e4m3", 0.05)
         want = (x[part, heads + 1:] / 0.04).to(k.dtype)
         assert torch.equal(v.view(torch.uint8)[page_of, :, place], want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("N", [196608, 200704, 1 << 19])
+@pytest.mark.parametrize("between", ["decode", "fork"])
+def test_one_workspace_for_calls_with_counters(between, N):
+    """Counters past 96 KiB would meet the other calls' lists and partial results."""
+    K = 256
+    w = torch.from_numpy(wl.q4k_weights(N, K, wl.rng(1)).reshape(-1)).to(DEV)
+    x = torch.empty(xq.xq_q8k_bytes(1, K), dtype=torch.uint8, device=DEV)
+    xq.xq_quantize_q8k(x, torch.randn(1, K, device=DEV), 1, K)
+    s = setup([3000], 8, 2, 128, 16, "bf16", "f32", "hnd")
+    refs, status = torch.zeros(s["k"].shape[0], dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    tables, lens = torch.full((30000, 4), -1, dtype=torch.int32, device=DEV), torch.zeros(30000, dtype=torch.int32, device=DEV)
+    ids = torch.arange(10000, dtype=torch.int32, device=DEV)
+    need = max(xq.xq_gemv_q4k_q8k_workspace_bytes(N), xq.xq_attn_decode_workspace_bytes(1, 8, s["kv"], 3000),
+               xq.xq_cache_workspace_bytes(s["k"].shape[0], 30000))
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    y, yq = torch.empty(N, device=DEV), torch.empty(xq.xq_q8k_bytes(1, N), dtype=torch.uint8, device=DEV)
+    want = torch.empty_like(yq)
+    for _ in range(3):
+        yq.fill_(0xa5)
+        xq.xq_gemv_q4k_q8k(y, yq, w, x, N, K, workspace=ws)
+        xq.xq_quantize_q8k(want, y, 1, N)
+        torch.cuda.synchronize()
+        assert torch.equal(yq.view(-1, 320)[:, :292], want.view(-1, 320)[:, :292])
+        if between == "decode":
+            decode(s, 0, 0, 3000, ws)
+            check_decode(s, [3000], 0, 0, "decode")
+        else:
+            xq.xq_cache_fork(s["kv"], refs, tables, lens, ids, ids + 10000, status, workspace=ws)

@@ -22,3 +22,9 @@ def test_scales_whose_product_overflows(name, scale, k_scale):
 def test_more_workgroups_than_a_launch_counts(name, change):
     s, err = call(name, change)
     assert s == SHAPE and "too many workgroups" in err, err
+
+
+def test_counters_stay_in_the_first_96_kib():
+    """Where every call that shares a workspace keeps what has to stay zero."""
+    sizes = [xq.xq_gemv_q4k_q8k_workspace_bytes(256 * n) for n in range(1, 16385)]
+    assert sizes == [128 * min(n, 768) for n in range(1, 16385)]
