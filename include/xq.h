@@ -21,9 +21,11 @@
  *    `workspace_bytes`; the matching *_workspace_bytes query gives the exact
  *    bytes a call needs (0: none, and then workspace may be NULL). The caller
  *    zeroes a workspace once before its first use; every call that completes
- *    leaves it ready for the next (its arrival counters back at zero), so one
- *    workspace serves any sequence of calls on one stream whose needs it
- *    covers. Calls that may run at the same time (different streams) need
+ *    leaves it ready for the next (its arrival counters, which lie in its
+ *    first 96 KiB, back at zero), so one workspace serves any sequence of
+ *    calls on one stream whose needs it covers; xq_gemm_q4k_id alone needs
+ *    one of its own, since its map begins at the first byte. Calls that may
+ *    run at the same time (different streams) need
  *    different workspaces. A NULL workspace where one is needed is refused
  *    with XQ_E_NULL, a short one with XQ_E_SHAPE, a misaligned one with
  *    XQ_E_ALIGN.
@@ -236,7 +238,8 @@ xq_status xq_gemm_q4k_small_m_noalloc(float *y, const void *w, const void *xq, i
  * own pair alone, so results do not depend on how pairs fall into tiles.
  *  workspace  the expert map (tile descriptors, the pairs grouped by
  *      expert, the tile counts): xq_gemm_q4k_id_workspace_bytes(n_tokens,
- *      n_used, n_experts) bytes (at most 4.3 MB), rewritten by every call.
+ *      n_used, n_experts) bytes (at most 4.3 MB), rewritten by every call
+ *      from the first byte: no call that keeps counters may share it.
  * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
  */
 xq_status xq_gemm_q4k_id(float *y, const void *slab, const void *xq, const int32_t *ids,
