@@ -680,7 +680,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       // are added up. The first of its loads go out ahead of those that the
       // factors wait for.
       constexpr int kAhead = 8;
-      const int quads = heads * DP / 4, teams = max(1, kThreads / quads);
+      const int quads = heads * DP / 4, teams = join_teams(kThreads, quads);
       const int team = tid % teams;
       f32x4 ahead[kAhead];
 #pragma unroll
@@ -724,11 +724,11 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
         if (teams > 1) {
           sums[tid] = x;
           __syncthreads();
-          if (team == 0)
+          if (join_adds(tid, teams, quads - q0))
             for (int i = 1; i < teams; ++i) x += sums[tid + i];
           __syncthreads();
         }
-        if (team == 0 && q < quads && d < a.dim) {
+        if (join_adds(tid, teams, quads - q0) && d < a.dim) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             store_from_f32(a.out + row_at(r, a.out_row, a.out_head), IO, d + i, x[i]);

@@ -1,6 +1,7 @@
 // kv_lanes.h — which elements of a token's row each lane of the single-token
-// attention kernel loads. Plain constant expressions: the kernel and a check on
-// the host, lane by lane, use the same ones.
+// attention kernel loads, and which threads add up its join. Plain constant
+// expressions: the kernel and a check on the host, lane by lane, use the same
+// ones.
 #pragma once
 
 namespace xq {
@@ -30,5 +31,12 @@ constexpr int decode_v_dim(int c, int l16, int dim) {
   const int d0 = (c * 16 + l16) * decode_v_dims(DP);
   return kFits || d0 < dim ? d0 : 0;
 }
+
+// The join's `quads` outputs of four, more than threads or fewer: a round's
+// thread t adds to output t / teams, every teams-th part, and the first thread
+// of each team then adds the team's sums (those of the `teams` threads from t
+// on). Threads past teams * quads have no output.
+constexpr int join_teams(int threads, int quads) { return threads > quads ? threads / quads : 1; }
+constexpr bool join_adds(int t, int teams, int quads) { return t % teams == 0 && t / teams < quads; }
 
 }  // namespace xq

@@ -1,5 +1,6 @@
-"""The single-token attention kernel's loads of a cache row, lane by lane on the
-host: every one lies inside its row, and together they are the whole row."""
+"""The single-token attention kernel on the host, lane by lane: its loads of a
+cache row lie inside the row, and together they are the whole row; its join's
+sums are of the workgroup's own threads, each of them added once."""
 import os
 import subprocess
 
@@ -39,7 +40,24 @@ static void check_pad(int dim) {
   check<DP, false>(dim);
 }
 
+static void join(int heads, int dp) {
+  const int threads = 256, quads = heads * dp / 4, teams = xq::join_teams(threads, quads);
+  int outputs = 0;
+  for (int q0 = 0; q0 < quads; q0 += threads / teams) {
+    char added[256] = {};
+    for (int t = 0; t < threads; ++t) {
+      if (!xq::join_adds(t, teams, quads - q0)) continue;
+      ++outputs;
+      for (int i = 0; i < teams; ++i)
+        if (t + i >= threads || added[t + i]++) std::printf("%d heads of %d: thread %d adds %d\n", heads, dp, t, t + i), ++bad;
+    }
+  }
+  if (outputs != quads) std::printf("%d heads of %d: %d of %d outputs\n", heads, dp, outputs, quads), ++bad;
+}
+
 int main() {
+  for (int heads = 1; heads <= 16; ++heads)
+    for (int dp = 64; dp <= 256; dp += 64) join(heads, dp);
   for (int dim = 16; dim <= 256; dim += 16) switch (xq::decode_dim_pad(dim)) {
       case 64: check_pad<64>(dim); break;
       case 128: check_pad<128>(dim); break;
