@@ -87,6 +87,15 @@ __device__ __forceinline__ float heads_sum(float v) {
   return v + __shfl_xor(v, 32, kWave);
 }
 
+// A wave's lanes see what they have left for each other in LDS. (No
+// instruction: a wave's LDS accesses keep their order; this keeps the
+// compiler's.)
+__device__ __forceinline__ void lanes_meet() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // Bits 0 .. n-1.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0 : n >= 32 ? ~0u : (1u << n) - 1; }
 
@@ -271,8 +280,10 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     // and its v is cleared.
     k_at = ok ? page * a.k_page16 + slot * a.k_tok16 : k_at;
     v_at = ok ? page * a.v_page16 + slot * a.v_tok16 : v_at;
+    lanes_meet();
     places[wave][0][lane % kTile] = k_at;
     places[wave][1][lane % kTile] = v_at;
+    lanes_meet();
     live = static_cast<uint32_t>(__ballot(ok));
   };
   u32x4 kr[2][KN], vr[VC][8];
