@@ -430,7 +430,8 @@ size_t xq_attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv *
  *           cache's type is io or XQ_E4M3. Strides and alignment as in
  *           xq_attn_decode. Rows of out that no sequence names stay as they are.
  *  starts   device int32[seqs + 1], ascending from >= 0 to <= rows; a
- *           sequence's part outside 0..rows or beyond max_chunk is left out.
+ *           sequence's part outside 0..rows or beyond max_chunk is left out,
+ *           and its other rows keep the positions that they have in the whole.
  *  max_chunk in 1..rows: the longest chunk; rows * heads <= 2^31 - 1, seqs <= 2^16,
  *  seqs * kv_heads * ceil(max_chunk * heads / kv_heads / 128) < 2^24. The cache,
  *  heads, scale, window and sinks as xq_attn_decode.

@@ -215,13 +215,18 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   int heads, head0, first_row = 0, pos = 0, pmin = 0, pmax = 0;
   if constexpr (CHUNK) {
     first_row = min(max(a.starts[seq], 0), a.rows);
-    const int count = min(min(max(a.starts[seq + 1], first_row), a.rows) - first_row, a.max_chunk);
+    const int end = a.starts[seq + 1];
+    const int count = min(min(max(end, first_row), a.rows) - first_row, a.max_chunk);
     head0 = ht * kHeadTile;
     heads = min(kHeadTile, count * a.group - head0);
     if (heads <= 0) return;
-    pos = n - count + static_cast<int>(div_by(head0 + min(l16, heads - 1), a.group_div));
-    pmin = n - count + static_cast<int>(div_by(head0, a.group_div));
-    pmax = n - count + static_cast<int>(div_by(head0 + heads - 1, a.group_div));
+    // The chunk's last row, whether it is done or left out, is the sequence's
+    // last token. A position below 0 sees nothing.
+    const int64_t base = static_cast<int64_t>(n) - end + first_row;
+    auto position = [&](int r) { return static_cast<int>(max(base + div_by(head0 + r, a.group_div), int64_t{-1})); };
+    pos = position(min(l16, heads - 1));
+    pmin = position(0);
+    pmax = position(heads - 1);
   } else {
     heads = min(kHeadTile, a.group - ht * kHeadTile);
     head0 = kvh * a.group + ht * kHeadTile;

@@ -139,25 +139,29 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
   const int seq = unit / a.kv_heads, kvh = unit % a.kv_heads;
 
   const int first = min(max(a.starts[seq], 0), a.rows);
-  const int count = min(min(max(a.starts[seq + 1], first), a.rows) - first, a.max_chunk);
+  const int end = a.starts[seq + 1];
+  const int count = min(min(max(end, first), a.rows) - first, a.max_chunk);
   const int group = a.group.d;
   const int row0 = tile * kRows;
   if (row0 >= count * group) return;
   const int n = static_cast<int>(min(static_cast<int64_t>(max(0, a.lens[seq])), a.table_tokens));
-  const int base = n - count;  // position of the chunk's first token; may be below 0
+  // Position of row first + t: the chunk's last row, whether it is done or left
+  // out, is the sequence's last token. One below 0 sees nothing.
+  const int64_t base = static_cast<int64_t>(n) - end + first;
+  auto position = [&](uint32_t t) { return static_cast<int>(max(base + t, int64_t{-1})); };
 
   // This lane's row.
   const int r = row0 + wave * 32 + l32;
   const bool mine = r < count * group;
   const int tok = mine ? div_by(r, a.group) : 0;
   const int head = kvh * group + (r - tok * group);
-  const int pos = mine ? base + tok : -1;
+  const int pos = mine ? position(tok) : -1;
   const int from = a.window ? pos - a.window : -1;  // sees j > from, or j < sinks
   const int sinks = a.window ? a.sinks : 0;
 
   // The workgroup's tokens: the sinks' tiles, then those from `lo` on.
-  const int pmin = base + div_by(row0, a.group);
-  const int pmax = base + div_by(min(row0 + kRows, count * group) - 1, a.group);
+  const int pmin = position(div_by(row0, a.group));
+  const int pmax = position(div_by(min(row0 + kRows, count * group) - 1, a.group));
   const int lo = a.window ? max(0, pmin - a.window + 1) / kTile * kTile : 0;
   const int ns = min(sinks, lo);
   const int sink_tiles = (ns + kTile - 1) / kTile;

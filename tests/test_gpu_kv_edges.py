@@ -6,7 +6,7 @@ import torch
 import kv_reference as ref
 import quantized_decode_mat_amd as xq
 import workloads as wl
-from test_gpu_kv_attention import _device, check_decode, check_prefill, decode, prefill, setup  # noqa: F401
+from test_gpu_kv_attention import _device, check_decode, check_prefill, compare, decode, expect, prefill, setup  # noqa: F401
 from test_gpu_kv_prefill_large import copies
 from test_gpu_kv_rope_pages import check_rope, freqs
 
@@ -121,3 +121,22 @@ def test_one_workspace_for_calls_with_counters(between, N):
             check_decode(s, [3000], 0, 0, "decode")
         else:
             xq.xq_cache_fork(s["kv"], refs, tables, lens, ids, ids + 10000, status, workspace=ws)
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("starts,most,window", [([3, 63], 25, 0), ([3, 63], 25, 20), ([-5, 40], 100, 0), ([20, 2000], 100, 0),
+                                                ([20, 2 ** 31 - 1], 100, 30), ([-2 ** 31, 2 ** 31 - 1], 100, 30), ([90, 115], 100, 6)])
+def test_rows_that_are_left_out_move_no_others(starts, most, window, many):
+    """Row i of a chunk of c has position n - c + i whatever part of the chunk is done."""
+    rows, n, seqs = 100, 90, 1 if not many else 300
+    s = setup([n] * seqs, 4, 2, 64, 16, "bf16", "bf16", "hnd", rows=rows)
+    # the sequences of the larger call have no rows but for the first
+    s["starts"] = torch.tensor(starts + [starts[1]] * (seqs - 1), dtype=torch.int32, device=DEV)
+    xq.xq_attn_prefill(s["out"], s["q"], s["kv"], s["table"], s["lens"], s["starts"], most, s["scale"], window=window, sinks=2)
+    torch.cuda.synchronize()
+    first = max(starts[0], 0)
+    done = torch.arange(first, max(first, min(starts[1], rows, first + most)), device=DEV)
+    pos = n - starts[1] + done
+    assert len(done) and ((s["full"] != 7.0).any(-1).any(-1).nonzero()[:, 0] == done).all()
+    want, mag, slack = expect(s, 0, slice(int(done[0]), int(done[-1]) + 1), pos, n, window, 2)
+    compare(s, s["out"][done], want, mag, slack, ref.half_step("bf16"), n, "part of a chunk")
