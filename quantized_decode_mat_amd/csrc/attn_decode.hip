@@ -221,9 +221,9 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     heads = min(kHeadTile, count * a.group - head0);
     if (heads <= 0) return;
     // The chunk's last row, whether it is done or left out, is the sequence's
-    // last token. A position below 0 sees nothing.
-    const int64_t base = static_cast<int64_t>(n) - end + first_row;
-    auto position = [&](int r) { return static_cast<int>(max(base + div_by(head0 + r, a.group_div), int64_t{-1})); };
+    // last token. A position below 0 sees nothing. (end > first_row >= 0 here.)
+    const int base = n - (end - first_row);
+    auto position = [&](int r) { return max(base + static_cast<int>(div_by(head0 + r, a.group_div)), -1); };
     pos = position(min(l16, heads - 1));
     pmin = position(0);
     pmax = position(heads - 1);

@@ -146,9 +146,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
   if (row0 >= count * group) return;
   const int n = static_cast<int>(min(static_cast<int64_t>(max(0, a.lens[seq])), a.table_tokens));
   // Position of row first + t: the chunk's last row, whether it is done or left
-  // out, is the sequence's last token. One below 0 sees nothing.
-  const int64_t base = static_cast<int64_t>(n) - end + first;
-  auto position = [&](uint32_t t) { return static_cast<int>(max(base + t, int64_t{-1})); };
+  // out, is the sequence's last token. One below 0 sees nothing. (end > first
+  // >= 0 here, so nothing leaves 32 bits; 64 would leave the scalar unit.)
+  const int base = n - (end - first);
+  auto position = [&](int t) { return max(base + t, -1); };
 
   // This lane's row.
   const int r = row0 + wave * 32 + l32;
@@ -172,11 +173,12 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
   u32x4 qf[DP / 16];
   {
     const uint8_t* qr = a.q + (first + tok) * a.q_row + head * a.q_head;
+    const bool reads = mine && !a.zero;
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s) {
       const int d0 = s * 16 + lh * 8;
       qf[s] = u32x4{0, 0, 0, 0};
-      if (mine && d0 < a.dim && !a.zero) qf[s] = *reinterpret_cast<const u32x4*>(qr + d0 * 2);
+      if (reads && (FULL || d0 < a.dim)) qf[s] = *reinterpret_cast<const u32x4*>(qr + d0 * 2);
       if (a.flip) qf[s] ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
     }
   }
