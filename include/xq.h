@@ -424,7 +424,9 @@ size_t xq_attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv *
  * nothing (a position below 0, pages that are missing) gives zeros. A token
  * that a row does not see has no influence on it, whatever its bytes are.
  * The weights p enter their product with v rounded to 16 bits (io's, or better
- * where the rows are few); sums and maxima are f32.
+ * where the rows are few; f16's 11 bits hold down to 2^-26 of a row's largest
+ * weight, and what is below is off by at most 2^-37 of it); sums and maxima are
+ * f32.
  *
  *  out, q   device [rows][heads][dim] of type io, XQ_BF16 or XQ_F16; the
  *           cache's type is io or XQ_E4M3. Strides and alignment as in

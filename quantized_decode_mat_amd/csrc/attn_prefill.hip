@@ -29,7 +29,7 @@
 //
 // Precision: S, the softmax and O are f32; q enters in its own 16 bits, an
 // 8-bit cache is widened exactly; p is rounded to 16 bits, as the product
-// needs.
+// needs (bf16 to 2^-8; f16 to 2^-11 down to 2^-26 of the row's maximum).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -275,11 +275,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-  // Weights are exp2(c s - ref). ref follows the row's maximum from below, by
-  // at most kLag: a weight is then at most 2^kLag, which neither its 16 bits
-  // nor the f32 sums mind, and the sums are hardly ever rescaled. `limit` is
-  // ref + kLag, or -infinity before the row's first token.
-  constexpr float kLag = 8.f;
+  // Weights are exp2(c s - ref). A new ref makes the row's maximum so far weigh
+  // 2^kLift, and stays until one weighs over 2^(kLift + kLag): the f32 sums do
+  // not mind, and are seldom rescaled. `limit` is the score that ends a ref,
+  // -infinity before the row's first token. In f16 the lift keeps small weights'
+  // bits: none is above 2^15, and those down to 2^-26 of the row's maximum are
+  // normal numbers. (Without it 131072 tokens of 2^-26 each, 2^-9 of the sum,
+  // added nothing to the product.)
+  constexpr float kLag = MT == kF16 ? 3.f : 8.f, kLift = MT == kF16 ? 12.f : 0.f;
   float ref = 0.f, limit = -INFINITY, l = 0.f;
 
   if (tid < 3) odd[tid] = 0;
@@ -365,11 +368,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     }
     const float top = halves_max(fmaxf(max16(st[0]), max16(st[1]))) * a.c;
     if (__ballot(top > limit)) {
-      const float to = top > limit ? top : ref;
+      const float to = top > limit ? top - kLift : ref;
       const float alpha = limit == -INFINITY ? 0.f : exp2_fast(ref - to);
       if (top > limit) {
         ref = to;
-        limit = to + kLag;
+        limit = top + kLag;
       }
       l *= alpha;
 #pragma unroll

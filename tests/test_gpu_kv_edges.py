@@ -140,3 +140,20 @@ def test_rows_that_are_left_out_move_no_others(starts, most, window, many):
     assert len(done) and ((s["full"] != 7.0).any(-1).any(-1).nonzero()[:, 0] == done).all()
     want, mag, slack = expect(s, 0, slice(int(done[0]), int(done[-1]) + 1), pos, n, window, 2)
     compare(s, s["out"][done], want, mag, slack, ref.half_step("bf16"), n, "part of a chunk")
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("io", ["bf16", "f16"])
+@pytest.mark.parametrize("strong", [5, 2000])
+def test_many_small_weights(io, many, strong):
+    """2047 tokens of 2^-26 the weight of one whose v is 0."""
+    n = copies([64], 4, 2) if many else 1
+    lens, chunks = [2048] * n, [64] * n
+    s = setup(lens, 4, 2, 64, 16, io, io, "hnd", rows=64 * n, poison=False)
+    s["q"].zero_(), s["k"].zero_()
+    s["v"].copy_(s["v"].float().abs())
+    s["q"][..., 0], s["scale"] = 1.0, 1.0
+    page = s["table"][:, strong // 16].long()
+    s["k"][page, :, strong % 16, 0], s["v"][page, :, strong % 16] = 18.0, 0.0
+    starts = prefill(s, chunks, 0, 0)
+    check_prefill(s, lens, chunks, starts, 0, 0, "small weights")
