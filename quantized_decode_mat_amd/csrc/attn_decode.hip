@@ -596,7 +596,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
           o[c][j] = mfma16<MT>(vf, pf[0], o[c][j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (fabsf(x[i]) < INFINITY) o[c][j][i] += x[i];
+            o[c][j][i] += fabsf(x[i]) < INFINITY ? x[i] : 0.f;
           __builtin_amdgcn_sched_barrier(0);
         }
       }

@@ -78,7 +78,9 @@ __device__ __forceinline__ u32x2 load_transposed(const uint8_t* p) {
 __device__ __forceinline__ f32x2 both_halves(float v) {
   const uint32_t u = __builtin_bit_cast(uint32_t, v);
   const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  const uint32_t x = s[0], y = s[1];  // a bit cast of s[1] itself takes s[0]
+  // (clang's bit cast of a vector's element reads the vector's start: that of
+  // s[1] itself would be s[0]'s.)
+  const uint32_t x = s[0], y = s[1];
   return f32x2{__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)};
 }
 __device__ __forceinline__ float halves_max(float v) {
@@ -361,9 +363,12 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t bits = static_cast<uint32_t>(mine >> (32 * h));
+        // A select, not a branch: set under a branch of several conditions,
+        // element 0 of a vector went wrong in the compiler's back end (the block
+        // that sets it came out empty; its store had moved ahead of a copy that
+        // undid it), and tokens 0 and 4 of a tile stayed visible.
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!(bits & (1u << (8 * (i / 4) + i % 4)))) st[h][i] = -INFINITY;
+        for (int i = 0; i < 16; ++i) st[h][i] = bits & (1u << (8 * (i / 4) + i % 4)) ? st[h][i] : -INFINITY;
       }
     }
     const float top = halves_max(fmaxf(max16(st[0]), max16(st[1]))) * a.c;
