@@ -362,7 +362,7 @@ enum { XQ_F32 = 0, XQ_BF16 = 1, XQ_F16 = 2, XQ_E4M3 = 3 };
  *  dtype  XQ_BF16, XQ_F16 or XQ_E4M3 (8 bits, 4 exponent, 3 mantissa, largest
  *         448, no infinity). What a stored k stands for is k * k_scale, a
  *         stored v is v * v_scale, in every type; both finite and above 0.
- *  1 <= layers, pages, page, kv_heads; pages * page <= 2^31 - 1 (a slot is an
+ *  1 <= layers <= 2^24; 1 <= pages, page; 1 <= kv_heads <= 2^20; pages * page <= 2^31 - 1 (a slot is an
  *  int32's worth; byte offsets are 64-bit). dim a multiple of 16, 16..256.
  *  k and v 16-byte aligned; strides >= 0 and multiples of 16 bytes.
  * Attention and the append work on one layer (layers = 1: a layer of a larger

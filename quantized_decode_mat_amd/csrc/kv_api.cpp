@@ -26,8 +26,9 @@ xq_status check_kv(const xq_kv* kv, bool one_layer) {
   if (!kv->v) return fail(XQ_E_NULL, "kv v is NULL");
   if (kv->dtype != XQ_BF16 && kv->dtype != XQ_F16 && kv->dtype != XQ_E4M3)
     return fail(XQ_E_SHAPE, "kv dtype=%d is none of XQ_BF16, XQ_F16, XQ_E4M3", kv->dtype);
-  if (kv->layers < 1 || kv->layers > kMaxInt)
-    return fail(XQ_E_SHAPE, "kv layers=%lld below 1", (long long)kv->layers);
+  // (layer, k or v, 1 of 64 parts) of a page is an int32 in the page moves.
+  if (kv->layers < 1 || kv->layers > (1 << 24))
+    return fail(XQ_E_SHAPE, "kv layers=%lld outside 1..2^24", (long long)kv->layers);
   if (one_layer && kv->layers != 1)
     return fail(XQ_E_SHAPE, "kv layers=%lld; this call takes one layer", (long long)kv->layers);
   if (kv->pages < 1 || kv->page < 1 || kv->pages > kMaxInt / kv->page)

@@ -28,3 +28,9 @@ def test_counters_stay_in_the_first_96_kib():
     """Where every call that shares a workspace keeps what has to stay zero."""
     sizes = [xq.xq_gemv_q4k_q8k_workspace_bytes(256 * n) for n in range(1, 16385)]
     assert sizes == [128 * min(n, 768) for n in range(1, 16385)]
+
+
+@pytest.mark.parametrize("name", ["xq_cache_copy", "xq_cache_free", "xq_cache_fork", "xq_cache_compact"])
+def test_more_layers_than_a_page_move_counts(name):
+    s, err = call(name, dict(kv_layers=(1 << 24) + 1))
+    assert s == SHAPE and "layers=16777217" in err, err
