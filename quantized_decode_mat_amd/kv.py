@@ -191,12 +191,12 @@ def _attention(out, q, kv):
 def xq_attn_decode(out, q, kv: xq_kv_cache, tables, lens, scale: float, window: int = 0, sinks: int = 0,
                    max_len: int = None, workspace=None, stream=None) -> None:
     """Attention of one new token per sequence; max_len (the longest length,
-    which the host knows) is the tables' room when left out."""
+    which the host knows) is the tables' room when left out, 2^30 at most."""
     op, qp, kind, seqs, heads, out_row, out_head, q_row, q_head = _attention(out, q, kv)
     index = kv.index
     tp, width, t_stride = _table(tables, "tables", index, seqs)
     if max_len is None:
-        max_len = width * kv.page
+        max_len = min(width * kv.page, 1 << 30)
     wp, wb = _workspace(workspace, index)
     _check(lib().xq_attn_decode(op, qp, kind, seqs, heads, out_row, out_head, q_row, q_head, kv._ref, tp,
                                 width, t_stride, _ints(lens, "lens", index, seqs), scale, window, sinks,

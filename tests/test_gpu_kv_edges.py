@@ -157,3 +157,13 @@ def test_many_small_weights(io, many, strong):
     s["k"][page, :, strong % 16, 0], s["v"][page, :, strong % 16] = 18.0, 0.0
     starts = prefill(s, chunks, 0, 0)
     check_prefill(s, lens, chunks, starts, 0, 0, "small weights")
+
+
+def test_tables_with_room_for_more_than_the_longest_length():
+    """max_len, left out, is the tables' room; 2^30 tokens are the most a call takes."""
+    s = setup([2000, 70], 4, 2, 64, 1024, "bf16", "f32", "hnd")
+    wide = torch.full((2, (1 << 20) + 3), -1, dtype=torch.int32, device=DEV)
+    wide[:, :s["table"].shape[1]] = s["table"]
+    ws = torch.zeros(xq.xq_attn_decode_workspace_bytes(2, 4, s["kv"], 1 << 30), dtype=torch.uint8, device=DEV)
+    xq.xq_attn_decode(s["out"], s["q"], s["kv"], wide, s["lens"], s["scale"], workspace=ws)
+    check_decode(s, [2000, 70], 0, 0, "wide tables")
