@@ -51,7 +51,6 @@ DOWN = (4096, 14336)
 COUNTERS = os.path.join(ROOT, "profiles", "hbm_traffic_counters.json")
 COUNTERS_MD = os.path.join(ROOT, "profiles", "hbm_traffic_counters.md")
 CSRC = os.path.join(ROOT, "quantized_decode_mat_amd", "csrc")
-BUILD_SCRIPT = os.path.join(ROOT, "quantized_decode_mat_amd", "build.py")
 # Each counted kernel: the name rocprofv3 reports (a prefix), the launches of a
 # --counters run, its algorithmic bytes per launch, and the sources its code
 # comes from (the summary is void once any of them changes).
@@ -135,12 +134,14 @@ def sha_of(path):
 
 
 def sources_sha(files):
-    """Hash of a kernel's sources and of the build script that sets its
-    compiler flags: either changes the machine code the counters measured."""
+    """Hash of a kernel's sources and of its compiler flags: either changes the
+    machine code the counters measured. (Other kernels' files do not.)"""
+    from quantized_decode_mat_amd import build
     h = hashlib.sha256()
-    for path in [os.path.join(CSRC, f) for f in files] + [BUILD_SCRIPT]:
+    for path in [os.path.join(CSRC, f) for f in files]:
         with open(path, "rb") as fh:
             h.update(fh.read())
+    h.update("\0".join(build.FLAGS).replace(build.ROOT, "").encode())
     return h.hexdigest()[:16]
 
 
