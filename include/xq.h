@@ -38,6 +38,9 @@
  *    refused). There is no fallback kernel.
  *  - The gates run before any HIP call in this order: null pointers, shape,
  *    alignment, then the device (it must be gfx950).
+ *  - A launch counts its threads in 32 bits. Sizes within an entry point's
+ *    bounds that would give a kernel 2^32 and more (a mat-vec of 2^26 rows of
+ *    at most 16 blocks, say) are refused with XQ_E_LAUNCH.
  *
  * Byte layouts (all little-endian):
  *  q8_K block, 320 B per 256 activations (section 25.2, the integer-route

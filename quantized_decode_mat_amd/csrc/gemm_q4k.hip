@@ -952,6 +952,7 @@ hipError_t launch_split(float* y, const void* w, const void* xq, int64_t M, int6
     part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kSplitCounterBytes);
   }
   const int grid = n_full + (tiles - n_full) * ks;
+  if (!countable(grid, kThreads)) return hipErrorInvalidConfiguration;
   // The 16-token tile computes little per super-block. On a grid of at most
   // one workgroup per CU (256), nothing else on the CU hides a super-block's
   // load, so its ring goes three deep: 4096x14336 at 7 and 16 tokens 14.3
@@ -1041,10 +1042,6 @@ hipError_t launch_gemm_q4k_id(float* y, const void* slab, const void* xq, const 
   int32_t* sorted = reinterpret_cast<int32_t*>(base + lay.sorted);
   int32_t* n_tiles = reinterpret_cast<int32_t*>(base + lay.counts);
   int32_t* n_small = n_tiles + 1;
-  hipError_t e;
-  if ((e = launch_route_experts(ids, n_pairs, n_experts, kIdBM, kIdBS, sorted, desc, n_tiles,
-                                desc_s, n_small, stream)) != hipSuccess)
-    return e;
   const int nb = static_cast<int>(K / 256);
   const int ntiles = static_cast<int>((rows + BN - 1) / BN);
   const int64_t expert_bytes = rows * nb * static_cast<int64_t>(kQ4KBytes);
@@ -1058,6 +1055,12 @@ hipError_t launch_gemm_q4k_id(float* y, const void* slab, const void* xq, const 
                       static_cast<int>(n_used), per_slot_x, expert_bytes};
   const IdGemm id_small{sorted, desc_s, n_small, static_cast<int>(n_experts),
                         static_cast<int>(n_used), per_slot_x, expert_bytes};
+  if (!countable(small_base + static_cast<int64_t>(small) * ntiles, kThreads))
+    return hipErrorInvalidConfiguration;
+  hipError_t e;
+  if ((e = launch_route_experts(ids, n_pairs, n_experts, kIdBM, kIdBS, sorted, desc, n_tiles,
+                                desc_s, n_small, stream)) != hipSuccess)
+    return e;
   hipLaunchKernelGGL(gemm_q4k_id_mixed_kernel, dim3(small_base + small * ntiles), dim3(kThreads),
                      0, stream, y, static_cast<const uint8_t*>(slab),
                      static_cast<const uint8_t*>(xq), static_cast<int>(n_pairs),
@@ -1110,7 +1113,7 @@ hipError_t launch_gemm_q4k_wave_split(float* y, const void* w, const void* xq, i
                                       int64_t N, int64_t K, hipStream_t stream) {
   const int mtiles = static_cast<int>((M + 15) / 16);
   const int64_t grid = (N + WsStage::kRows - 1) / WsStage::kRows * mtiles;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!countable(grid, kThreads)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(gemm_q4k_wave_split_kernel, dim3(static_cast<unsigned>(grid)),
                      dim3(kThreads), 0, stream, y, static_cast<const uint8_t*>(w),
                      static_cast<const uint8_t*>(xq), static_cast<int>(M), static_cast<int>(N),

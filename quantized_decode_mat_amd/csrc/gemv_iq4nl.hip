@@ -379,6 +379,7 @@ template <int PF, int FMT, bool GACT = false>
 hipError_t launch_staged(float* y, const uint8_t* w, const uint8_t* xq, int N, int bpr, int prefix,
                          int64_t row_bytes, int nq8, const IdArgs& id, hipStream_t stream) {
   const int grid = (N + kWavesPerGroup - 1) / kWavesPerGroup;
+  if (!countable(grid, kThreads)) return hipErrorInvalidConfiguration;
   const size_t lds = GACT ? 0 : static_cast<size_t>(nq8) * kQ8KBytes;
   if (id.sel)
     hipLaunchKernelGGL((gemv_iq4nl_kernel<1, PF, true, FMT, GACT>), dim3(grid, id.used),

@@ -498,6 +498,7 @@ hipError_t launch_cfg(float* y, const uint8_t* w, const uint8_t* xq, int N, int 
                       const IdArgs& id, hipStream_t stream) {
   const int waves = (N + R - 1) / R;
   const int grid = (waves + W - 1) / W;
+  if (!countable(grid, W * kWave)) return hipErrorInvalidConfiguration;
   const size_t lds = GACT ? 0 : static_cast<size_t>(nb) * kQ8KBytes;
   if (id.sel)
     hipLaunchKernelGGL((gemv_q4k_kernel<R, PF, W, NA, CLAMP, true, false, GACT>),
@@ -556,6 +557,7 @@ hipError_t launch_multi_cfg(float* y, const uint8_t* w, const uint8_t* xq, int N
                             int tokens, hipStream_t stream) {
   const int waves = (N + R - 1) / R;
   const int grid = (waves + W - 1) / W;
+  if (!countable(grid, W * kWave)) return hipErrorInvalidConfiguration;
   const size_t lds = static_cast<size_t>(tokens) * nb * kQ8KBytes;
   hipLaunchKernelGGL((gemv_q4k_multi_kernel<TM, R, PF, W, NA, CLAMP>), dim3(grid),
                      dim3(W * kWave), lds, stream, y, w, xq, N, nb, tokens);
@@ -584,6 +586,7 @@ hipError_t launch_unit_split(float* y, const uint8_t* w, const uint8_t* xq, int 
   const int units = (nb + kUnitBlocks - 1) / kUnitBlocks;
   if (units < 1 || units > kSplitMaxUnits || tokens < 1 || tokens > TM)
     return hipErrorInvalidValue;
+  if (!countable((N + R - 1) / R, units * kWave)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((gemv_q4k_unit_split_kernel<TM, R>), dim3((N + R - 1) / R),
                      dim3(units * kWave), 0, stream, y, w, xq, N, nb, tokens);
   return hipGetLastError();

@@ -39,6 +39,7 @@ hipError_t launch_quantize_q8k(void* xq, const float* x, int64_t rows, int64_t K
                                hipStream_t stream) {
   const int64_t nblocks = rows * (K / 256);
   const int64_t grid = (nblocks + 3) / 4;
+  if (!countable(grid, 256)) return hipErrorInvalidConfiguration;
   // K is a multiple of 256, so every row starts as aligned as x.
   if (reinterpret_cast<uintptr_t>(x) % 16 == 0)
     hipLaunchKernelGGL(q8k_quantize_kernel<true>, dim3(static_cast<uint32_t>(grid)), dim3(256), 0,

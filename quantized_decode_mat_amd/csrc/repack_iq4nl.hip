@@ -173,6 +173,7 @@ hipError_t launch_repack_iq4nl(void* resident, const void* file_blocks, int64_t 
     // The tiled form (16-byte aligned source). Its indices: block and row
     // indices below block_base + n, tile indices below n / 256.
     const int64_t tiles = (n + kTileBlocks - 1) / kTileBlocks;
+    if (!countable(tiles, kRepackThreads)) return hipErrorInvalidConfiguration;
     const bool t32 = block_base + n < (int64_t{1} << 32);
     const uint8_t* s8 = static_cast<const uint8_t*>(file_blocks);
     if (row_aligned) {
@@ -200,6 +201,7 @@ hipError_t launch_repack_iq4nl(void* resident, const void* file_blocks, int64_t 
   }
   // 32-bit indices when the largest of them (the grid's items, the last
   // global block) fits below 2^32.
+  if (!countable(grid, kRepackThreads)) return hipErrorInvalidConfiguration;
   const int64_t kI32 = int64_t{1} << 32;
   const bool idx32 = grid * kRepackThreads < kI32 && block_base + n < kI32;
   if (row_aligned) {

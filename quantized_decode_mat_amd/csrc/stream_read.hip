@@ -59,6 +59,7 @@ hipError_t launch_stream_read(const void* buf, int64_t bytes, uint32_t* sink,
                               hipStream_t stream) {
   const int64_t n16 = bytes / 16;
   const int grid = static_cast<int>(stream_read_sink_words(bytes));
+  if (!countable(stream_read_sink_words(bytes), kThreads)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(stream_read_kernel, dim3(grid), dim3(kThreads), 0, stream,
                      static_cast<const uint4*>(buf), n16, sink);
   return hipGetLastError();

@@ -12,6 +12,11 @@ namespace xq {
 // from global memory instead.
 constexpr int64_t kMaxStagedK = 49152;
 
+// A launch counts its threads in 32 bits, and more wrap round without an
+// error (few workgroups run, most outputs stay unwritten): a launcher whose
+// grid grows with the call's sizes asks first.
+inline bool countable(int64_t groups, int64_t threads) { return groups * threads < (int64_t{1} << 32); }
+
 // Three launchers take a caller-owned device workspace (`ws`, `ws_bytes`):
 // the split-K partials and arrival counters of the small-M product, the
 // arrival counters of the fused quantizing mat-vec, and the grouped
