@@ -387,9 +387,11 @@ typedef struct {
  *   out[b][h] = sum_j p_j * v_scale * v_j[g],
  *   p = softmax over the visible j of scale * k_scale * (q[b][h] . k_j[g]).
  * A sequence with no visible token gives zeros; a visible infinity or NaN in v
- * reaches the dims that it is in (in k, a NaN of every dim). Sums, maxima and products are
- * held in f32; q and the weights p enter the matrix instructions as two or
- * three 16-bit pieces where one would round them below the output's type.
+ * reaches the dims that it is in. In k a NaN makes every dim NaN, and so does an
+ * infinity but where it makes the score minus infinity, which weighs nothing.
+ * Sums, maxima and products are held in f32; q and the weights p enter the
+ * matrix instructions as two or three 16-bit pieces where one would round them
+ * below the output's type.
  *
  *  out, q   device [seqs][heads][dim] of type io (XQ_F32, XQ_BF16, XQ_F16),
  *           strides per sequence (row) and head, both a multiple of 16 bytes;
@@ -403,7 +405,11 @@ typedef struct {
  *  window in 0..2^30 (0: none), sinks in 0..2^30 (read only with a window).
  *  max_len in 1..2^30: no length is above it (longer ones are clamped); the split of
  *  the work is planned for it, the result of a given plan is the same from
- *  call to call, bit for bit.
+ *  call to call, bit for bit. Fewer than 768 (sequence, kv head, 16 heads) units
+ *  (1536 of up to 64 dims, or of up to 128 of an 8-bit cache whose pages'
+ *  heads lie apart) share the work
+ *  evenly whatever their lengths; from there on a unit is one workgroup's, and a
+ *  sequence much longer than the others is the call's time.
  *  workspace  the splits' partial results and arrival counters:
  *      xq_attn_decode_workspace_bytes(...) bytes with the same arguments
  *      (0 when the plan does not split), zeroed before first use.
@@ -426,6 +432,9 @@ size_t xq_attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv *
  * j > p - window, or j < sinks). The sum is xq_attn_decode's. A row that sees
  * nothing (a position below 0, pages that are missing) gives zeros. A token
  * that a row does not see has no influence on it, whatever its bytes are.
+ * A tile of a chunk's rows is one workgroup's for all the tokens that it sees:
+ * a few new tokens on a long context keep few compute units busy (8 on 131072
+ * with 8 kv heads take 1.3 ms, 16 of 256 units).
  * The weights p enter their product with v rounded to 16 bits (io's, or better
  * where the rows are few; f16's 11 bits hold down to 2^-26 of a row's largest
  * weight, and what is below is off by at most 2^-37 of it); sums and maxima are

@@ -29,8 +29,8 @@
 // both slower.)
 //
 // Measured: 2 sequences of up to 131072, 32 heads of 128 dims on 8 kv heads, bf16
-// cache: 163-171 us, 6.0-6.3 TB/s (a streaming read: 7.3); 64 windows of 8192 of
-// 8 bits 132-138 us; one sequence of 517 11.2 us, of which the join is 3.6.
+// cache: 163-172 us, 6.0-6.3 TB/s (a streaming read: 7.3); 64 windows of 8192 of
+// 8 bits 131-134 us; one sequence of 517 11.0 us, of which the join is 3.6.
 //
 // Precision: q and the weights p enter the 16-bit matrix instructions as sums
 // of pieces (each the rounded remainder of the one before). For a 16-bit
@@ -777,7 +777,11 @@ struct Plan {
 // join (3.6 us) for each sequence that crosses from one range to the next. Up
 // to three steps (384 tokens) one workgroup is faster than a join: 300 tokens
 // take 10.4 against 11.2 us, 517 tokens 13 against 11.2. With three and more
-// units for each such workgroup, one unit each is even enough.
+// units for each such workgroup, one unit each is even enough where the lengths
+// are alike (32 heads on 8 kv heads of 128 dims, bf16: 128 sequences of 2000 178
+// us, 5.9 TB/s, as 95 of them that share; 256 of 500 to 4000 380 us, 6.1 TB/s)
+// and far from it where one is much longer: 96 sequences, one of 131072 and 95
+// of 1000, take 1.38 ms, with 94 of 1000, shared, 161 us.
 Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t window,
           int64_t sinks) {
   Plan p;
@@ -912,10 +916,14 @@ hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t se
 
 // Tiles of 16 rows, each walked by a workgroup's four waves in steps of 128
 // tokens, against tiles of 128 rows in steps of 64: as long as all of the
-// former are on the card at once they are the shorter walk. 11 new tokens on
-// 1530 (8 bits) 25 against 73 us, 364 on 624 with 8 heads 18 against 26, 90 on
-// 1976 of 192 dims 26 against 39; but 8 on 92 of 192 dims 16.5 against 12. The
-// batch of 7 chunks of up to 300 on 4 kv heads of 4 has 2100 and stays there.
+// former are on the card at once (two a CU) they are the shorter walk, whatever
+// its length. bf16, 32 heads on 8 kv heads of 128 dims: 11 new tokens on 1530 26
+// against 47 us, 8 on 131072 1.33 against 3.53 ms, 256 on 131072 (512 tiles)
+// 2.69 against 3.54; 512 on 131072 5.31 against 3.56. 8 heads on 2: 364 on 624
+// 17.5 against 25 us, 90 on 1976 of 192 dims 47 against 89. A walk of a single
+// step is the exception, 8 on 92 of 192 dims 15.5 against 12. Neither kernel
+// shares one tile's tokens between workgroups: 8 on 131072 are 16 workgroups
+// that read 0.4 TB/s, where single tokens on the whole card read 6.
 bool chunk_in_rows(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_chunk) {
   return seqs * chunk_units(heads, kv, max_chunk) <= 512;
 }

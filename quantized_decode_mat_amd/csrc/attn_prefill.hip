@@ -20,10 +20,13 @@
 //    per lane), in the same order of the summed index. O^T's column is again
 //    row l % 32: rescaling is local to the lane.
 //
-// Measured: 4096 tokens, 32 heads of 128 dims on 8 kv heads, bf16: 171-179 us,
-// 768-804 TFLOP/s (64% of a large library product's rate); MFMA busy 37%, VALU
-// issue 47% of the cycles, a third of the waves' time in waits. 8192 tokens with
-// a window of 2048, f16: 329-339 us. What made it so: operands read ahead of
+// Measured: 4096 tokens, 32 heads of 128 dims on 8 kv heads, bf16: 168-196 us by
+// card, 701-818 TFLOP/s (56-66% of a large library product's rate); of the
+// cycles MFMA are busy in 37%, VALU in 46%, LDS in 55%, and a third of the waves'
+// time is waits. The tile's ceiling is LDS: every wave reads the whole of K and V
+// for its 32 rows, as many cycles as its matrix instructions take, and writes
+// are a quarter on top. 8192 tokens with a window of 2048, f16: 323-341 us. What
+// made it so: operands read ahead of
 // the matrix instructions (256 -> 230 us with the lagging reference, 199 with
 // both), wave priority over them (183). Few rows run elsewhere: chunk_in_rows.
 //

@@ -127,7 +127,9 @@ class xq_rope_plan:
 
 def _raw_stream(stream, index: int):
     """The caller's stream, or the current one of the tensors' device, which
-    has to be the current device."""
+    has to be the current device. (What torch.cuda.current_device and
+    current_stream look up, without the objects they make: 0.2 against
+    1.4 us a call.)"""
     if torch._C._cuda_getDevice() != index:
         raise ValueError("the tensors are on device %d, the current device is %d"
                          % (index, torch._C._cuda_getDevice()))
