@@ -43,7 +43,8 @@ def test_what_lies_beside_a_row_has_no_influence(cache, io, dim):
 
 @pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("cache,io,scale,k_scale", [("bf16", "bf16", 0.0, 1.0), ("f16", "f16", 0.0, 1.0),
-                                                   ("e4m3", "bf16", 0.0, 0.75), ("e4m3", "f16", 1e-30, 1e-20)])
+                                                   ("e4m3", "bf16", 0.0, 0.75), ("e4m3", "f16", 1e-30, 1e-20),
+                                                   ("bf16", "bf16", 1e-39, 1.0), ("f16", "f16", -1e-39, 1.0)])
 def test_scale_of_zero(cache, io, scale, k_scale, many):
     """Every visible token weighs the same."""
     n = copies([64, 129], 4, 2) if many else 1
