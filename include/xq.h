@@ -353,7 +353,7 @@ int64_t xq_repack_dword_prefix_launches(void);
  */
 
 /* Element types. */
-enum { XQ_F32 = 0, XQ_BF16 = 1, XQ_F16 = 2, XQ_E4M3 = 3 };
+enum { XQ_F32 = 0, XQ_BF16 = 1, XQ_F16 = 2, XQ_E4M3 = 3, XQ_E2M1 = 4 };
 
 /*
  * A paged cache, a host struct that describes device memory. Token j of a
@@ -362,9 +362,22 @@ enum { XQ_F32 = 0, XQ_BF16 = 1, XQ_F16 = 2, XQ_E4M3 = 3 };
  *   k + l * k_stride[0] + p * k_stride[1] + h * k_stride[2] + s * k_stride[3] + d
  * (v the same with v_stride), so pages stored head by head or token by token
  * are both just strides.
- *  dtype  XQ_BF16, XQ_F16 or XQ_E4M3 (8 bits, 4 exponent, 3 mantissa, largest
- *         448, no infinity). What a stored k stands for is k * k_scale, a
- *         stored v is v * v_scale, in every type; both finite and above 0.
+ *  dtype  XQ_BF16, XQ_F16, XQ_E4M3 (8 bits, 4 exponent, 3 mantissa, largest
+ *         448, no infinity) or XQ_E2M1 (4 bits, below). What a stored k stands
+ *         for is k * k_scale, a stored v is v * v_scale, in every type; both
+ *         finite and above 0.
+ *  XQ_E2M1: an element is a sign (bit 3) and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *  (bits 0..2, in that order), two to a byte, the even dim in the low bits,
+ *  times a power of two that 32 consecutive dims of a row share: a byte,
+ *  exponent + 127. dim is a multiple of 32; strides still count elements. The
+ *  powers of layer l, page p, head h, slot s are dim / 32 bytes at
+ *   k_exp + l * k_exp_stride[0] + p * k_exp_stride[1] + h * k_exp_stride[2] + s * k_exp_stride[3]
+ *  (bytes; v_exp the same), of a row of 4 bytes up to 128 dims and of 8 beyond,
+ *  whose rest has no meaning; bases and strides 4-byte aligned. The append
+ *  stores powers 2^-23 .. 2^13 (bytes 104..140), which every call reads exactly,
+ *  and 255 for a block that holds a NaN, all of which then are NaN. Of other
+ *  bytes those up to 250 are read as what they stand for, but in a chunk's
+ *  attention with XQ_F16 as f16 holds it. Other types do not read these fields.
  *  1 <= layers <= 2^24; 1 <= pages, page; 1 <= kv_heads <= 2^20; pages * page <= 2^31 - 1 (a slot is an
  *  int32's worth; byte offsets are 64-bit). dim a multiple of 16, 16..256.
  *  k and v 16-byte aligned; strides >= 0 and multiples of 16 bytes.
@@ -377,6 +390,8 @@ typedef struct {
     int64_t k_stride[4], v_stride[4];
     int32_t dtype;
     float k_scale, v_scale;
+    void *k_exp, *v_exp;
+    int64_t k_exp_stride[4], v_exp_stride[4];
 } xq_kv;
 
 /*
@@ -441,7 +456,7 @@ size_t xq_attn_decode_workspace_bytes(int64_t seqs, int64_t heads, const xq_kv *
  * f32.
  *
  *  out, q   device [rows][heads][dim] of type io, XQ_BF16 or XQ_F16; the
- *           cache's type is io or XQ_E4M3. Strides and alignment as in
+ *           cache's type is io, XQ_E4M3 or XQ_E2M1. Strides and alignment as in
  *           xq_attn_decode. Rows of out that no sequence names stay as they are.
  *  starts   device int32[seqs + 1], ascending from >= 0 to <= rows; a
  *           sequence's part outside 0..rows or beyond max_chunk is left out,
@@ -493,7 +508,12 @@ xq_status xq_rope(void *out, int32_t out_type, int64_t out_row, int64_t out_head
  * The same rotation of q and k, fused with the append of k and v to the
  * cache: q_out = rope(q); token t's rope(k) / k_scale and v / v_scale go to
  * slot slots[t] (page slots[t] / page, place slots[t] % page), rounded once to
- * the cache's type (XQ_E4M3: clamped to +-448). A slot outside
+ * the cache's type (XQ_E4M3: clamped to +-448). XQ_E2M1: a block of 32 takes
+ * the smallest power of two 2^e, e in -23..13, by which its largest |x| is
+ * below 7 (so that it rounds to 6 at most), and each x / 2^e is rounded to the
+ * nearest of the eight values, ties to the even code, above 6 to 6; rotation
+ * and division are carried in f64 there, so that a value next to a border
+ * between two codes falls on its own side. A slot outside
  * 0..pages*page-1 writes nothing to the cache. No two tokens may have the same
  * slot.
  *  q, k, v  device [tokens][heads or kv_heads][dim] of one type x_type (XQ_F32,
@@ -507,6 +527,22 @@ xq_status xq_rope_append(void *q_out, int32_t out_type, int64_t out_row, int64_t
                          int64_t v_row, int64_t v_head, int32_t x_type, int64_t tokens,
                          int64_t heads, const int32_t *pos, int64_t pos_stride,
                          const xq_rope_freqs *rope, const int64_t *slots, void *stream);
+
+/*
+ * Tokens of a cache as values, for what looks into it or takes it elsewhere:
+ * k_out[t][h] = k * k_scale and v_out[t][h] = v * v_scale of slot slots[t]
+ * (page slots[t] / page, place slots[t] % page), in f32 and rounded once to
+ * out_type. A slot outside 0..pages*page-1 gives zeros; a slot may be named
+ * more than once.
+ *  k_out, v_out  device [tokens][kv_heads][dim] of type out_type (XQ_F32,
+ *         XQ_BF16, XQ_F16), each with its own strides, aligned to their
+ *         elements. slots device int64[tokens].
+ *  tokens >= 1, tokens * kv_heads <= 2^31 - 1; one layer.
+ * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
+ */
+xq_status xq_cache_read(void *k_out, int64_t k_row, int64_t k_head, void *v_out, int64_t v_row,
+                        int64_t v_head, int32_t out_type, const xq_kv *kv, const int64_t *slots,
+                        int64_t tokens, void *stream);
 
 /*
  * The pages of a cache, all its layers at once. refs[p] counts the table

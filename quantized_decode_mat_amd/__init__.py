@@ -94,11 +94,12 @@ def lib() -> ctypes.CDLL:
             L.xq_attn_prefill.argtypes = [P, P, S, I, I, I, I, I, I, I, P, P, I, I, P, P, I, F, I, I, P]
             L.xq_rope.argtypes = [P, S, I, I, P, S, I, I, I, I, I, P, I, P, S, P]
             L.xq_rope_append.argtypes = [P, S, I, I, P, P, I, I, P, I, I, P, I, I, S, I, I, P, I, P, P, P]
+            L.xq_cache_read.argtypes = [P, I, I, P, I, I, S, P, P, I, P]
             L.xq_cache_copy.argtypes = [P, P, P, I, P]
             L.xq_cache_free.argtypes = [P, P, P, I, I, I, P, P, I, P]
             L.xq_cache_fork.argtypes = [P, P, P, I, I, I, P, P, P, I, P, P, Z, P]
             L.xq_cache_compact.argtypes = [P, P, P, I, I, I, P, P, Z, P]
-            for f in ("xq_attn_decode", "xq_attn_prefill", "xq_rope", "xq_rope_append", "xq_cache_copy",
+            for f in ("xq_attn_decode", "xq_attn_prefill", "xq_rope", "xq_rope_append", "xq_cache_read", "xq_cache_copy",
                       "xq_cache_free", "xq_cache_fork", "xq_cache_compact"):
                 getattr(L, f).restype = S
             L.xq_attn_decode_workspace_bytes.argtypes = [I, I, P, I, I, I]
@@ -301,6 +302,6 @@ def xq_bench_stream_read(buf, nbytes: int, sink, stream=None) -> None:
 
 
 from .kv import (  # noqa: E402  (they use the helpers above)
-    XQ_BF16, XQ_E4M3, XQ_F16, XQ_F32, xq_attn_decode, xq_attn_decode_workspace_bytes,
-    xq_attn_prefill, xq_cache_compact, xq_cache_copy, xq_cache_fork, xq_cache_free,
+    XQ_BF16, XQ_E2M1, XQ_E4M3, XQ_F16, XQ_F32, xq_attn_decode, xq_attn_decode_workspace_bytes,
+    xq_attn_prefill, xq_cache_compact, xq_cache_copy, xq_cache_fork, xq_cache_free, xq_cache_read,
     xq_cache_workspace_bytes, xq_kv_cache, xq_rope, xq_rope_append, xq_rope_plan)

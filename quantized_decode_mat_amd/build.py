@@ -42,6 +42,7 @@ SOURCES = [
     "attn_prefill.hip",
     "rope.hip",
     "kv_pages.hip",
+    "kv_read.hip",
     "xq_api.cpp",
     "kv_api.cpp",
 ]

@@ -38,10 +38,12 @@
 // many pieces as f32 has bits (three of bf16's 8, two of f16's 11). The
 // instructions wait on memory, so the pieces cost no time.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_device.h"
 #include "kv_lanes.h"
 #include "kv_launch.h"
+#include "kv_view.h"
 
 namespace xq {
 namespace {
@@ -75,6 +77,7 @@ struct DecodeArgs {
   FastDiv ranges;  // parts that the sequences' steps are shared out to
   float c;        // scale * k_scale * log2(e)
   float v_scale;
+  ExpView exps;
 };
 
 // Sum and maximum over the four lanes that hold one head.
@@ -109,8 +112,10 @@ __device__ __forceinline__ u32x4 load_words(const uint8_t* p) {
   } else if constexpr (BYTES == 8) {
     const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
     return u32x4{v.x, v.y, 0, 0};
-  } else {
+  } else if constexpr (BYTES == 4) {
     return u32x4{__builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)), 0, 0, 0};
+  } else {
+    return u32x4{__builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(p)), 0, 0, 0};
   }
 }
 
@@ -121,7 +126,7 @@ __device__ __forceinline__ u32x4 load_words(const uint8_t* p) {
 // the loads: 64 windows of 8192 150 -> 138 us, 32 sequences of up to 4099 40 ->
 // 33.5. (With pages stored token by token, where a workgroup's rows lie apart,
 // the latter lose: 131072 tokens x 2 89 -> 100 us; those take one.)
-constexpr int groups_per_cu(int ct, int dp) { return dp == 64 || (ct == kE4M3 && dp == 128) ? 2 : 1; }
+constexpr int groups_per_cu(int ct, int dp) { return dp == 64 || ((ct == kE4M3 || ct == kE2M1) && dp == 128) ? 2 : 1; }
 
 // CT: the cache's type. IO: q's and out's. DP: dim rounded up to 64, 128, 192
 // or 256; FULL: dim is DP. CHUNK: several new tokens per sequence; a
@@ -129,23 +134,28 @@ constexpr int groups_per_cu(int ct, int dp) { return dp == 64 || (ct == kE4M3 &&
 // see different tokens.
 template <int CT, int IO, int DP, bool FULL, bool CHUNK>
 __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_kernel(DecodeArgs a) {
-  constexpr int MT = CT == kBF16 ? kBF16 : kF16;   // the matrix instruction's type
-  constexpr int EB = CT == kE4M3 ? 1 : 2;
+  constexpr bool F4 = CT == kE2M1;
+  constexpr int MT = CT == kBF16 || F4 ? kBF16 : kF16;  // the matrix instruction's type
+  constexpr int EB = CT == kE4M3 ? 1 : 2;               // (not of 4 bits)
   constexpr int IB = IO == kF32 ? 4 : 2;
   // Pieces of q and of p.
-  constexpr int NQ = MT == kBF16 ? (IO == kBF16 ? 1 : 3) : (IO == kF32 ? 2 : 1);
+  constexpr int NQ = MT == kBF16 ? (IO == kBF16 ? 1 : F4 && IO == kF16 ? 2 : 3) : (IO == kF32 ? 2 : 1);
   constexpr int NP = MT == kBF16 && IO == kF32 ? 3 : 2;
   constexpr int QS = DP / 32;                      // instructions of S^T along dim
   // 16 bytes of K give KL instructions their operand: an 8-bit row's are 16
   // dims, two instructions' worth.
-  constexpr int KL = CT == kE4M3 ? 2 : 1;
-  constexpr int KN = decode_k_loads(DP, EB);       // K loads of a lane per token
+  constexpr int KL = F4 ? decode4_k_bytes(DP) / 4 : CT == kE4M3 ? 2 : 1;
+  constexpr int KN = F4 ? decode4_k_loads(DP) : decode_k_loads(DP, EB);  // K loads of a lane per token
   static_assert(KN * KL == QS);
   constexpr int VE = decode_v_dims(DP);            // dims of a lane's V load
   constexpr int VC = decode_v_loads(DP);
+  constexpr int VB = F4 ? VE / 2 : VE * EB;        // its bytes
+  constexpr int NE = DP > 128 ? 2 : 1;             // dwords of a row's exponents
   constexpr int OS = DP + 4;                       // floats of a joined row in LDS
   extern __shared__ float lds[];
   __shared__ __attribute__((aligned(16))) uint32_t places[kWaves][2][kTile];
+  // Exponents of a tile's rows of k and of v.
+  __shared__ __attribute__((aligned(16))) uint32_t powers[F4 ? kWaves : 1][2][NE][kTile];
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int l16 = lane % 16, lg = lane / 16;
@@ -275,6 +285,14 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   };
   uint32_t live;  // bit t: token t of the tile is there
   uint32_t k_at = 0, v_at = 0;
+  // Of 4 bits: lanes 0..31 read the exponents of k for the tile's tokens, the
+  // others those of v.
+  const uint8_t* eb = nullptr;
+  const uint8_t* e_at = nullptr;
+  if constexpr (F4) {
+    eb = lane < kTile ? a.exps.k + kvh * a.exps.k_head : a.exps.v + kvh * a.exps.v_head;
+    e_at = eb;
+  }
   auto place = [&](int u0, int page) {
     const int u = u0 + lane % kTile;
     const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.kv.pages);
@@ -285,13 +303,19 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     // and its v is cleared.
     k_at = ok ? page * a.k_page16 + slot * a.k_tok16 : k_at;
     v_at = ok ? page * a.v_page16 + slot * a.v_tok16 : v_at;
+    if constexpr (F4)
+      e_at = ok ? eb + page * (lane < kTile ? a.exps.k_page : a.exps.v_page) +
+                      slot * (lane < kTile ? a.exps.k_tok : a.exps.v_tok)
+                : e_at;
     lanes_meet();
     places[wave][0][lane % kTile] = k_at;
     places[wave][1][lane % kTile] = v_at;
     lanes_meet();
     live = static_cast<uint32_t>(__ballot(ok));
   };
-  u32x4 kr[2][KN], vr[VC][8];
+  u32x4 kr[2][KN];
+  std::conditional_t<F4, uint32_t, u32x4> vr[VC][8];
+  uint32_t er[NE];  // of 4 bits: this lane's row of exponents
   auto load_k = [&]() {
     uint32_t at[2];
 #pragma unroll
@@ -300,8 +324,23 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     for (int t = 0; t < 2; ++t) {
       const uint8_t* p = kb + static_cast<uint64_t>(at[t]) * 16;
 #pragma unroll
-      for (int s = 0; s < KN; ++s)
-        kr[t][s] = *reinterpret_cast<const u32x4*>(p + decode_k_dim<DP, FULL>(s, lg, EB, a.dim) * EB);
+      for (int s = 0; s < KN; ++s) {
+        if constexpr (!F4) {
+          kr[t][s] = *reinterpret_cast<const u32x4*>(p + decode_k_dim<DP, FULL>(s, lg, EB, a.dim) * EB);
+        } else {
+          const uint8_t* row = p + decode4_k_dim<DP, FULL>(s, lg, a.dim) / 2;
+          if constexpr (KL == 4) {
+            kr[t][s] = *reinterpret_cast<const u32x4*>(row);
+          } else {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(row);
+            kr[t][s] = u32x4{w.x, w.y, 0, 0};
+          }
+        }
+      }
+    }
+    if constexpr (F4) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) er[i] = reinterpret_cast<const uint32_t*>(e_at)[i];
     }
   };
   auto load_v = [&]() {
@@ -313,18 +352,25 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     for (int t = 0; t < 8; ++t) {
       const uint8_t* p = vb + static_cast<uint64_t>(at[t / 4][t % 4]) * 16;
 #pragma unroll
-      for (int c = 0; c < VC; ++c)  // (what stands for dims past the end nothing uses)
-        vr[c][t] = load_words<VE * EB>(p + decode_v_dim<DP, FULL>(c, l16, a.dim) * EB);
+      for (int c = 0; c < VC; ++c) {  // (what stands for dims past the end nothing uses)
+        const int d0 = decode_v_dim<DP, FULL>(c, l16, a.dim);
+        if constexpr (F4) vr[c][t] = load_words<VB>(p + d0 / 2).x;
+        else vr[c][t] = load_words<VB>(p + d0 * EB);
+      }
     }
   };
-  auto widen_v = [&](const u32x4(&r)[8], u32x4(&w)[8]) {
+  // Of 4 bits: the powers of the lane's eight tokens of V, for its dims.
+  float vp[VC][8];
+  auto widen_v = [&](int c, u32x4(&w)[8]) {
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      if constexpr (CT == kE4M3) {
-        const u32x2 x = widen4<MT>(r[t].x), y = widen4<MT>(r[t].y);
+      if constexpr (F4) {
+        w[t] = widen8<MT>(vr[c][t], vp[c][t]);
+      } else if constexpr (CT == kE4M3) {
+        const u32x2 x = widen4<MT>(vr[c][t].x), y = widen4<MT>(vr[c][t].y);
         w[t] = u32x4{x.x, x.y, y.x, y.y};
       } else {
-        w[t] = r[t];
+        w[t] = vr[c][t];
       }
     }
   };
@@ -348,9 +394,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     float x[QS][8];
     float top = 0.f;
     const uint8_t* qr = a.q + row_at(min(l16, heads - 1), a.q_row, a.q_head);
-    auto q_dim = [&](int s) {
-      return KL == 1 ? s * 32 + lg * 8 : (s / 2) * 64 + lg * 16 + (s % 2) * 8;
-    };
+    auto q_dim = [&](int s) { return (s / KL * 4 + lg) * 8 * KL + s % KL * 8; };
     u32x4 raw[QS][IB / 2];
 #pragma unroll
     for (int s = 0; s < QS; ++s) {
@@ -415,6 +459,32 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   // many are under way and waits for no more than it needs.
   while (u0 < end) {  // wave-uniform
     const uint32_t here = live;
+    float kp[2][KN];  // of 4 bits: the powers of the lane's K
+    if constexpr (F4) {
+      // The rows' exponents go through LDS to the lanes that hold their codes.
+      lanes_meet();
+#pragma unroll
+      for (int i = 0; i < NE; ++i) powers[wave][lane / kTile][i][lane % kTile] = er[i];
+      lanes_meet();
+      constexpr int kBlocks = KL == 4 ? 1 : 2;  // K loads of a block
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int s = 0; s < KN; ++s) {
+          const int b = (s * 4 + lg) / kBlocks;
+          kp[t][s] = block_power((powers[wave][0][NE == 1 ? 0 : b / 4][t * 16 + l16] >> (b % 4 * 8)) & 0xff);
+        }
+#pragma unroll
+      for (int c = 0; c < VC; ++c) {
+        const int b = min((c * 16 + l16) * VE / 32, DP / 32 - 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const u32x4 e = *reinterpret_cast<const u32x4*>(&powers[wave][1][NE == 1 ? 0 : b / 4][t * 16 + lg * 4]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vp[c][t * 4 + i] = block_power((e[i] >> (b % 4 * 8)) & 0xff);
+        }
+      }
+    }
     f32x4 st[2] = {zero4, zero4};
 #pragma unroll
     for (int s = 0; s < QS; ++s)
@@ -423,7 +493,9 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           u32x4 kf;
-          if constexpr (KL == 2) {
+          if constexpr (F4) {
+            kf = widen8<MT>(kr[t][s / KL][s % KL], kp[t][s / KL]);
+          } else if constexpr (KL == 2) {
             const u32x4 w = kr[t][s / 2];
             const u32x2 x = widen4<MT>(w[(s % 2) * 2]), y = widen4<MT>(w[(s % 2) * 2 + 1]);
             kf = u32x4{x.x, x.y, y.x, y.y};
@@ -432,7 +504,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
           }
           if constexpr (!FULL) {
             // q is 0 past the end, but 0 * infinity is not.
-            const int d0 = KL == 1 ? s * 32 + lg * 8 : (s / 2) * 64 + lg * 16 + (s % 2) * 8;
+            const int d0 = (s / KL * 4 + lg) * 8 * KL + s % KL * 8;
             if (d0 >= a.dim) kf = u32x4{0, 0, 0, 0};
           }
           st[t] = mfma16<MT>(kf, qf[s][p], st[t]);
@@ -508,13 +580,26 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       for (int t = 0; t < 8; ++t)
         if (!((here >> ((t / 4) * 16 + lg * 4 + t % 4)) & 1))
 #pragma unroll
-          for (int c = 0; c < VC; ++c) vr[c][t] = u32x4{0, 0, 0, 0};
+          for (int c = 0; c < VC; ++c) {
+            vr[c][t] = {};
+            if constexpr (F4) vp[c][t] = 0.f;
+          }
     }
     // Whether the tile's V has an infinity or NaN: an exponent of all ones (of
     // 8 bits, all ones but the sign) carries into the sign's place. (An 8-bit V
     // has no infinity, and a NaN that every row sees needs no care.)
     bool odd = false;
-    if (CT != kE4M3 || !same) {
+    if constexpr (F4) {
+      // (Of 4 bits as of 8: a NaN by a block's power alone.)
+      if (CHUNK && !same) {
+        bool any = false;
+#pragma unroll
+        for (int c = 0; c < VC; ++c)
+#pragma unroll
+          for (int t = 0; t < 8; ++t) any |= vp[c][t] == INFINITY;
+        odd = __ballot(any) != 0;
+      }
+    } else if (CT != kE4M3 || !same) {
       uint32_t carry = 0;
 #pragma unroll
       for (int c = 0; c < VC; ++c)
@@ -530,13 +615,18 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
       for (int c = 0; c < VC; ++c)
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < 8; ++t) {
+          if constexpr (F4) {
+            if (vp[c][t] == INFINITY) vp[c][t] = 0.f, vr[c][t] = 0;
+          } else {
 #pragma unroll
-          for (int i = 0; i < VE * EB / 4; ++i) {
-            const uint32_t w = vr[c][t][i];
-            const uint32_t ones = (((w & ~kSigns) + kOne) & kSigns) >> (8 * EB - 1);
-            vr[c][t][i] = w & ~(ones * (EB == 1 ? 0xffu : 0xffffu));
+            for (int i = 0; i < VE * EB / 4; ++i) {
+              const uint32_t w = vr[c][t][i];
+              const uint32_t ones = (((w & ~kSigns) + kOne) & kSigns) >> (8 * EB - 1);
+              vr[c][t][i] = w & ~(ones * (EB == 1 ? 0xffu : 0xffffu));
+            }
           }
+        }
       odd = false;
 #pragma unroll 1
       for (int k = 0; k < kTile; ++k) {
@@ -545,11 +635,23 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
         const uint32_t j = token_of(u0 + k), slot = j - div_by(j, a.kv.page) * a.kv.page.d;
         const uint8_t* row = vb + page0 * a.kv.v_page + slot * a.kv.v_tok;
         const bool in = (sees >> k) & 1;
+        if constexpr (F4) {
+          const uint8_t* exps = a.exps.v + kvh * a.exps.v_head + page0 * a.exps.v_page + slot * a.exps.v_tok;
+#pragma unroll
+          for (int c = 0; c < VC; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool nan = exps[decode_v_dim<DP, FULL>(c, lg * 4 + i, a.dim) / 32] == 0xff;
+#pragma unroll
+              for (int e = 0; e < VE; ++e) o[c][e][i] += in && nan ? __builtin_nanf("") : 0.f;
+            }
+          continue;
+        }
 #pragma unroll
         for (int c = 0; c < VC; ++c)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            u32x4 w = load_words<VE * EB>(row + decode_v_dim<DP, FULL>(c, lg * 4 + i, a.dim) * EB);
+            u32x4 w = load_words<VB>(row + decode_v_dim<DP, FULL>(c, lg * 4 + i, a.dim) * EB);
             if constexpr (EB == 1) {
               const u32x2 x = widen4<MT>(w.x), y = widen4<MT>(w.y);
               w = u32x4{x.x, x.y, y.x, y.y};
@@ -568,7 +670,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
         u32x4 vw[8];
-        widen_v(vr[c], vw);
+        widen_v(c, vw);
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
           const u32x4 vf = turned(vw, j, 0);
@@ -586,7 +688,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
         u32x4 vw[8];
-        widen_v(vr[c], vw);
+        widen_v(c, vw);
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
           const u32x4 vf = turned(vw, j, flip);
@@ -856,12 +958,10 @@ namespace {
 DecodeArgs fill(const RowsView& out, const RowsView& q, int64_t heads, const xq_kv& kv,
                 const TableView& tables, const int32_t* lens, float scale, int64_t window,
                 int64_t sinks) {
-  const int eb = elem_bytes(kv.dtype), ib = elem_bytes(q.type);
+  const int ib = elem_bytes(q.type);
   DecodeArgs a = {};
-  a.kv = KvView{static_cast<uint8_t*>(kv.k), static_cast<uint8_t*>(kv.v),
-                kv.k_stride[1] * eb, kv.k_stride[2] * eb, kv.k_stride[3] * eb,
-                kv.v_stride[1] * eb, kv.v_stride[2] * eb, kv.v_stride[3] * eb,
-                fast_div(static_cast<uint32_t>(kv.page)), static_cast<int>(kv.pages)};
+  a.kv = kv_view(kv);
+  a.exps = exp_view(kv);
   a.q = static_cast<const uint8_t*>(q.data);
   a.out = static_cast<uint8_t*>(out.data);
   a.tables = tables.data;
@@ -910,7 +1010,8 @@ hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t se
   switch (kv.dtype) {
     case kBF16: return launch_io<kBF16>(q.type, a, p, stream);
     case kF16: return launch_io<kF16>(q.type, a, p, stream);
-    default: return launch_io<kE4M3>(q.type, a, p, stream);
+    case kE4M3: return launch_io<kE4M3>(q.type, a, p, stream);
+    default: return launch_io<kE2M1>(q.type, a, p, stream);
   }
 }
 
@@ -944,6 +1045,9 @@ hipError_t launch_attn_chunk(const RowsView& out, const RowsView& q, int64_t row
   a.group_div = fast_div(static_cast<uint32_t>(a.group));
   if (kv.dtype == kBF16) return launch_dim<kBF16, kBF16, true>(a, p, stream);
   if (kv.dtype == kF16) return launch_dim<kF16, kF16, true>(a, p, stream);
+  if (kv.dtype == kE2M1)
+    return q.type == kBF16 ? launch_dim<kE2M1, kBF16, true>(a, p, stream)
+                           : launch_dim<kE2M1, kF16, true>(a, p, stream);
   return q.type == kBF16 ? launch_dim<kE4M3, kBF16, true>(a, p, stream)
                          : launch_dim<kE4M3, kF16, true>(a, p, stream);
 }

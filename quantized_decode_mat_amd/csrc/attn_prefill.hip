@@ -39,6 +39,7 @@
 
 #include "kv_device.h"
 #include "kv_launch.h"
+#include "kv_view.h"
 
 namespace xq {
 namespace {
@@ -65,6 +66,7 @@ struct PrefillArgs {
   int zero;       // q counts as 0, for a scale of 0 (c is 1 then: -infinity hides a score only if c > 0)
   float c;        // |scale| * k_scale * log2(e)
   float v_scale;
+  ExpView exps;
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -108,11 +110,12 @@ __device__ __forceinline__ float halves_sum(float v) {
   return s.x + s.y;
 }
 
-// MT: q's and out's type. CT: the cache's, MT or kE4M3. DP: dim rounded up to
+// MT: q's and out's type. CT: the cache's, MT, kE4M3 or kE2M1. DP: dim rounded up to
 // 64, 96, 128, 192 or 256; FULL: dim is DP.
 template <int MT, int CT, int DP, bool FULL>
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kernel(PrefillArgs a) {
-  constexpr int EB = CT == kE4M3 ? 1 : 2;
+  constexpr bool F4 = CT == kE2M1;
+  constexpr int EB = CT == kE4M3 ? 1 : 2;    // (not of 4 bits)
   // Bytes of a row in LDS. A row of K begins 4 banks past the one before, so 8
   // rows of a 16-byte column hit 32 banks; a row of V 8 banks (of 32 mod 128
   // bytes), so the 4 rows x 32 bytes of a transposing load do.
@@ -124,6 +127,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
   constexpr uint32_t kInf2 = MT == kBF16 ? 0x7f80u : 0x7c00u;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ uint32_t places[3][2][kTile];   // of a tile's tokens in k and v, in 16-byte units
+  __shared__ uint64_t powers_at[F4 ? 3 : 1][2][kTile];  // of 4 bits: of their exponents, in bytes
   __shared__ uint64_t found[3];              // bit t: token t of the tile is there
   __shared__ int odd[3];                     // a masked tile's V holds infinities or NaN
 
@@ -205,11 +209,18 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     const uint32_t slot = j - div_by(j, a.kv.page) * a.kv.page.d;
     places[t % 3][0][lane] = ok ? page * a.k_page16 + slot * a.k_tok16 : 0;
     places[t % 3][1][lane] = ok ? page * a.v_page16 + slot * a.v_tok16 : 0;
+    if constexpr (F4) {
+      powers_at[t % 3][0][lane] = ok ? page * a.exps.k_page + slot * a.exps.k_tok : 0;
+      powers_at[t % 3][1][lane] = ok ? page * a.exps.v_page + slot * a.exps.v_tok : 0;
+    }
     const uint64_t all = __ballot(ok);
     if (lane == 0) found[t % 3] = all;
   };
-  using Raw = std::conditional_t<EB == 2, u32x4, u32x2>;
+  using Raw = std::conditional_t<F4, uint32_t, std::conditional_t<EB == 2, u32x4, u32x2>>;
   Raw kr[PER], vr[PER];
+  uint32_t ke[PER], ve[PER];  // of 4 bits: the pieces' exponents
+  const uint8_t* keb = F4 ? a.exps.k + kvh * a.exps.k_head : nullptr;
+  const uint8_t* veb = F4 ? a.exps.v + kvh * a.exps.v_head : nullptr;
   auto load = [&](int t) {
     uint32_t at[2][PER];
 #pragma unroll
@@ -221,13 +232,17 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int d0 = (tid + i * kThreads) % CH * 8;
-        const uint8_t* p = (w ? vb : kb) + static_cast<uint64_t>(at[w][i]) * 16 +
-                           (FULL || d0 < a.dim ? d0 : 0) * EB;
+        const int d = FULL || d0 < a.dim ? d0 : 0;
+        const uint8_t* p = (w ? vb : kb) + static_cast<uint64_t>(at[w][i]) * 16 + (F4 ? d / 2 : d * EB);
         (w ? vr[i] : kr[i]) = *reinterpret_cast<const Raw*>(p);
+        if constexpr (F4)
+          (w ? ve[i] : ke[i]) = ((w ? veb : keb) + powers_at[t % 3][w][(tid + i * kThreads) / CH])[d / 32];
       }
   };
-  auto widen = [&](Raw w) {
-    if constexpr (EB == 2) {
+  auto widen = [&](Raw w, uint32_t e) {
+    if constexpr (F4) {
+      return widen8<MT>(w, block_power(e));
+    } else if constexpr (EB == 2) {
       return w;
     } else {
       const u32x2 x = widen4<MT>(w.x), y = widen4<MT>(w.y);
@@ -248,7 +263,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = tid + i * kThreads, row = at / CH, c = at % CH;
-      u32x4 w = widen(kr[i]);
+      u32x4 w = widen(kr[i], ke[i]);
       // q is 0 past the end, but 0 * infinity is not.
       if (!FULL && c * 8 >= a.dim) w = u32x4{0, 0, 0, 0};
       *reinterpret_cast<u32x4*>(kl + row * KB + c * 16) = w;
@@ -256,7 +271,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int at = tid + i * kThreads, row = at / CH, c = at % CH;
-      u32x4 w = widen(vr[i]);
+      u32x4 w = widen(vr[i], ve[i]);
       if (masked) {
         // 0 * infinity must not reach a row that does not see the token: such
         // values are left out here and added to the rows that do.
@@ -271,7 +286,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
       }
       *reinterpret_cast<u32x4*>(vl + row * VB + c * 16) = w;
       // (Widened one after the other: registers are short.)
-      if constexpr (EB == 1) __builtin_amdgcn_sched_barrier(0);
+      if constexpr (EB == 1 || F4) __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -440,9 +455,13 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             const int dim = d * 32 + 8 * (i / 4) + first_dim;
-            const uint8_t* p = row + (FULL || dim < a.dim ? dim : 0) * EB;
+            const int d0 = FULL || dim < a.dim ? dim : 0;
+            const uint8_t* p = row + (F4 ? d0 / 2 : d0 * EB);
             u32x2 w;
-            if constexpr (EB == 2) w = *reinterpret_cast<const u32x2*>(p);
+            if constexpr (F4) {
+              const u32x4 x = widen8<MT>(*reinterpret_cast<const uint16_t*>(p), block_power((veb + powers_at[t % 3][1][k])[d0 / 32]));
+              w = u32x2{x.x, x.y};
+            } else if constexpr (EB == 2) w = *reinterpret_cast<const u32x2*>(p);
             else w = widen4<MT>(*reinterpret_cast<const uint32_t*>(p));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -521,12 +540,9 @@ hipError_t launch_attn_prefill(const RowsView& out, const RowsView& q, int64_t r
   if (chunk_in_rows(seqs, heads, kv, max_chunk))
     return launch_attn_chunk(out, q, rows, seqs, heads, kv, tables, lens, starts, max_chunk, scale, window, sinks,
                              stream);
-  const int eb = elem_bytes(kv.dtype);
   PrefillArgs a;
-  a.kv = KvView{static_cast<uint8_t*>(kv.k), static_cast<uint8_t*>(kv.v),
-                kv.k_stride[1] * eb, kv.k_stride[2] * eb, kv.k_stride[3] * eb,
-                kv.v_stride[1] * eb, kv.v_stride[2] * eb, kv.v_stride[3] * eb,
-                fast_div(static_cast<uint32_t>(kv.page)), static_cast<int>(kv.pages)};
+  a.kv = kv_view(kv);
+  a.exps = exp_view(kv);
   a.q = static_cast<const uint8_t*>(q.data);
   a.out = static_cast<uint8_t*>(out.data);
   a.tables = tables.data;
@@ -558,6 +574,8 @@ hipError_t launch_attn_prefill(const RowsView& out, const RowsView& q, int64_t r
   if (a.zero) a.c = 1.f;
   a.v_scale = kv.v_scale;
   const uint32_t blocks = static_cast<uint32_t>(attn_prefill_blocks(seqs, heads, kv, max_chunk));
+  if (kv.dtype == kE2M1)
+    return q.type == kBF16 ? launch_dim<kBF16, kE2M1>(a, blocks, stream) : launch_dim<kF16, kE2M1>(a, blocks, stream);
   if (q.type == kBF16)
     return kv.dtype == kBF16 ? launch_dim<kBF16, kBF16>(a, blocks, stream)
                              : launch_dim<kBF16, kE4M3>(a, blocks, stream);

@@ -24,8 +24,10 @@ xq_status check_kv(const xq_kv* kv, bool one_layer) {
   if (!kv) return fail(XQ_E_NULL, "kv is NULL");
   if (!kv->k) return fail(XQ_E_NULL, "kv k is NULL");
   if (!kv->v) return fail(XQ_E_NULL, "kv v is NULL");
-  if (kv->dtype != XQ_BF16 && kv->dtype != XQ_F16 && kv->dtype != XQ_E4M3)
-    return fail(XQ_E_SHAPE, "kv dtype=%d is none of XQ_BF16, XQ_F16, XQ_E4M3", kv->dtype);
+  if (kv->dtype < XQ_BF16 || kv->dtype > XQ_E2M1)
+    return fail(XQ_E_SHAPE, "kv dtype=%d is none of XQ_BF16, XQ_F16, XQ_E4M3, XQ_E2M1", kv->dtype);
+  if (kv->dtype == XQ_E2M1 && !kv->k_exp) return fail(XQ_E_NULL, "kv k_exp is NULL");
+  if (kv->dtype == XQ_E2M1 && !kv->v_exp) return fail(XQ_E_NULL, "kv v_exp is NULL");
   // (layer, k or v, 1 of 64 parts) of a page is an int32 in the page moves.
   if (kv->layers < 1 || kv->layers > (1 << 24))
     return fail(XQ_E_SHAPE, "kv layers=%lld outside 1..2^24", (long long)kv->layers);
@@ -38,12 +40,18 @@ xq_status check_kv(const xq_kv* kv, bool one_layer) {
     return fail(XQ_E_SHAPE, "kv kv_heads=%lld outside 1..2^20", (long long)kv->kv_heads);
   if (kv->dim < 16 || kv->dim > 256 || kv->dim % 16)
     return fail(XQ_E_SHAPE, "kv dim=%lld not a multiple of 16 in 16..256", (long long)kv->dim);
+  if (kv->dtype == XQ_E2M1 && kv->dim % 32)
+    return fail(XQ_E_SHAPE, "kv dim=%lld of XQ_E2M1 not a multiple of 32", (long long)kv->dim);
   if (!(kv->k_scale > 0.f) || !(kv->v_scale > 0.f) || !std::isfinite(kv->k_scale) ||
       !std::isfinite(kv->v_scale))
     return fail(XQ_E_SHAPE, "kv scales %g, %g not finite and above 0", kv->k_scale, kv->v_scale);
   for (int i = 0; i < 4; ++i)
     if (kv->k_stride[i] < 0 || kv->v_stride[i] < 0)
       return fail(XQ_E_SHAPE, "kv stride %d is negative", i);
+  if (kv->dtype == XQ_E2M1)
+    for (int i = 0; i < 4; ++i)
+      if (kv->k_exp_stride[i] < 0 || kv->v_exp_stride[i] < 0)
+        return fail(XQ_E_SHAPE, "kv exponents' stride %d is negative", i);
   return XQ_OK;
 }
 
@@ -51,8 +59,16 @@ xq_status align_kv(const xq_kv* kv) {
   if (!aligned(kv->k, 16)) return fail(XQ_E_ALIGN, "kv k not 16-byte aligned");
   if (!aligned(kv->v, 16)) return fail(XQ_E_ALIGN, "kv v not 16-byte aligned");
   for (int i = 0; i < 4; ++i)
-    if (kv->k_stride[i] * type_bytes(kv->dtype) % 16 || kv->v_stride[i] * type_bytes(kv->dtype) % 16)
+    if (kv->k_stride[i] % (16 / xq::cache_bytes(2, kv->dtype) * 2) ||
+        kv->v_stride[i] % (16 / xq::cache_bytes(2, kv->dtype) * 2))
       return fail(XQ_E_ALIGN, "kv stride %d not a multiple of 16 bytes", i);
+  if (kv->dtype == XQ_E2M1) {
+    if (!aligned(kv->k_exp, 4)) return fail(XQ_E_ALIGN, "kv k_exp not 4-byte aligned");
+    if (!aligned(kv->v_exp, 4)) return fail(XQ_E_ALIGN, "kv v_exp not 4-byte aligned");
+    for (int i = 0; i < 4; ++i)
+      if (kv->k_exp_stride[i] % 4 || kv->v_exp_stride[i] % 4)
+        return fail(XQ_E_ALIGN, "kv exponents' stride %d not a multiple of 4 bytes", i);
+  }
   return XQ_OK;
 }
 
@@ -88,7 +104,7 @@ xq_status check_attention(int64_t heads, const xq_kv* kv, float scale, int64_t w
     // The kernels find a token by its place within a head, in 16-byte units.
     const double last = static_cast<double>(kv->pages - 1) * static_cast<double>(st[1]) +
                         static_cast<double>(kv->page - 1) * static_cast<double>(st[3]);
-    if (last * type_bytes(kv->dtype) >= 68719476736.0)
+    if (last * static_cast<double>(xq::cache_bytes(2, kv->dtype)) / 2 >= 68719476736.0)
       return fail(XQ_E_SHAPE, "kv pages of one layer reach over 64 GiB");
   }
   if (window < 0 || window > kMaxLen)
@@ -176,8 +192,8 @@ xq_status xq_attn_prefill(void *out, const void *q, int32_t io, int64_t rows, in
   if (io != XQ_BF16 && io != XQ_F16)
     return fail(XQ_E_SHAPE, "io=%d is neither XQ_BF16 nor XQ_F16", io);
   if (xq_status s = check_kv(kv, true)) return s;
-  if (kv->dtype != io && kv->dtype != XQ_E4M3)
-    return fail(XQ_E_SHAPE, "kv dtype=%d is neither io=%d nor XQ_E4M3", kv->dtype, io);
+  if (kv->dtype != io && kv->dtype != XQ_E4M3 && kv->dtype != XQ_E2M1)
+    return fail(XQ_E_SHAPE, "kv dtype=%d is neither io=%d nor XQ_E4M3 or XQ_E2M1", kv->dtype, io);
   if (xq_status s = check_attention(heads, kv, scale, window, sinks)) return s;
   if (rows < 1 || rows > kMaxInt / heads)
     return fail(XQ_E_SHAPE, "rows*heads = %lld*%lld outside 1..2^31-1", (long long)rows,
@@ -313,6 +329,31 @@ xq_status xq_rope_append(void *q_out, int32_t out_type, int64_t out_row, int64_t
                                   &vr, tokens, heads, kv->dim, kv, pos, pos_stride, *rope, false,
                                   slots, static_cast<hipStream_t>(stream)),
                   "xq_rope_append");
+}
+
+xq_status xq_cache_read(void *k_out, int64_t k_row, int64_t k_head, void *v_out, int64_t v_row,
+                        int64_t v_head, int32_t out_type, const xq_kv *kv, const int64_t *slots,
+                        int64_t tokens, void *stream) {
+  if (!k_out) return fail(XQ_E_NULL, "k_out is NULL");
+  if (!v_out) return fail(XQ_E_NULL, "v_out is NULL");
+  if (!slots) return fail(XQ_E_NULL, "slots is NULL");
+  if (!row_type(out_type))
+    return fail(XQ_E_SHAPE, "out_type=%d is none of XQ_F32, XQ_BF16, XQ_F16", out_type);
+  if (xq_status s = check_kv(kv, true)) return s;
+  if (tokens < 1 || tokens > kMaxInt / kv->kv_heads)
+    return fail(XQ_E_SHAPE, "tokens*kv_heads = %lld*%lld outside 1..2^31-1", (long long)tokens,
+                (long long)kv->kv_heads);
+  if (xq_status s = check_strides(k_row, k_head, "k_out")) return s;
+  if (xq_status s = check_strides(v_row, v_head, "v_out")) return s;
+  if (xq_status s = align_elems(k_out, out_type, "k_out")) return s;
+  if (xq_status s = align_elems(v_out, out_type, "v_out")) return s;
+  if (xq_status s = align_kv(kv)) return s;
+  if (!aligned(slots, 8)) return fail(XQ_E_ALIGN, "slots not 8-byte aligned");
+  if (xq_status s = check_device()) return s;
+  return launched(xq::launch_cache_read(xq::RowsView{k_out, out_type, k_row, k_head},
+                                        xq::RowsView{v_out, out_type, v_row, v_head}, *kv, slots, tokens,
+                                        static_cast<hipStream_t>(stream)),
+                  "xq_cache_read");
 }
 
 xq_status xq_cache_copy(const xq_kv *kv, const int32_t *src, const int32_t *dst, int64_t n,

@@ -18,9 +18,9 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // The element types of the C ABI (XQ_F32, ...).
-enum ElemType : int { kF32 = 0, kBF16 = 1, kF16 = 2, kE4M3 = 3 };
+enum ElemType : int { kF32 = 0, kBF16 = 1, kF16 = 2, kE4M3 = 3, kE2M1 = 4 };
 
-__host__ __device__ constexpr int elem_bytes(int t) { return t == kF32 ? 4 : t == kE4M3 ? 1 : 2; }
+__host__ __device__ constexpr int elem_bytes(int t) { return t == kF32 ? 4 : t == kE4M3 ? 1 : 2; }  // (not kE2M1)
 
 // x / d for 0 <= x < 2^31: multiplier floor(2^(31+s)/d) + 1 with
 // s = ceil(log2 d). Its excess over 2^(31+s)/d is at most 1, so the quotient's
@@ -61,6 +61,26 @@ __device__ __forceinline__ u32x2 widen4(uint32_t w) {
   else
     return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true))};
+}
+
+// A block's power of two from its byte (exponent + 127; 255, NaN, becomes
+// infinity, by which the conversions give NaN).
+__device__ __forceinline__ float block_power(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
+
+// Eight 4-bit values (one dword) times their block's power of two as 16-bit
+// ones: exact in bf16, and in f16 for the powers that the append stores.
+template <int T>
+__device__ __forceinline__ u32x4 widen8(uint32_t w, float power) {
+  if constexpr (T == kBF16)
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, power, 3))};
+  else
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, power, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, power, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, power, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, power, 3))};
 }
 
 // 16x16x32: A row / B column l % 16, 8 of the 32 from 8 * (l / 16); D column
@@ -110,6 +130,14 @@ struct KvView {
   int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;
   FastDiv page;
   int pages;
+};
+
+// The exponents of a layer of a 4-bit cache; strides in bytes. Null for other
+// types.
+struct ExpView {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;
 };
 
 }  // namespace xq

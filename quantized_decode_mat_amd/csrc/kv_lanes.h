@@ -20,6 +20,15 @@ constexpr int decode_k_dim(int s, int lg, int elem_bytes, int dim) {
   return FULL || d0 < dim ? d0 : 0;
 }
 
+// Of 4 bits: 16 bytes, or 8 where the padded row is no multiple of 128 dims.
+constexpr int decode4_k_bytes(int dp) { return dp % 128 ? 8 : 16; }
+constexpr int decode4_k_loads(int dp) { return dp / (8 * decode4_k_bytes(dp)); }
+template <int DP, bool FULL>
+constexpr int decode4_k_dim(int s, int lg, int dim) {
+  const int d0 = (s * 4 + lg) * 2 * decode4_k_bytes(DP);
+  return FULL || d0 < dim ? d0 : 0;
+}
+
 // V: 16 lanes take decode_v_dims elements each, decode_v_loads times. The last
 // round of 192 dims has lanes past even a full row's end (16 x 8 x 2 is 256):
 // only where the rounds fill the row is no comparison needed.

@@ -15,6 +15,13 @@ struct RowsView {
   int type;
   int64_t row, head;
 };
+// What n elements of a cache's type take (two of XQ_E2M1 share a byte), and a
+// row's exponents there: a byte for 32 dims, in rows of 4 or 8.
+inline int64_t cache_bytes(int64_t n, int32_t dtype) {
+  return dtype == XQ_E2M1 ? n / 2 : dtype == XQ_E4M3 ? n : 2 * n;
+}
+inline int64_t exp_row_bytes(int64_t dim) { return dim <= 128 ? 4 : 8; }
+
 struct TableView {
   const int32_t* data;
   int64_t width, stride;
@@ -45,6 +52,8 @@ hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k
                        int64_t tokens, int64_t heads, int64_t dim, const xq_kv* kv,
                        const int32_t* pos, int64_t pos_stride, const xq_rope_freqs& rope,
                        bool inverse, const int64_t* slots, hipStream_t stream);
+hipError_t launch_cache_read(const RowsView& k_out, const RowsView& v_out, const xq_kv& kv,
+                             const int64_t* slots, int64_t tokens, hipStream_t stream);
 hipError_t launch_cache_copy(const xq_kv& kv, const int32_t* src, const int32_t* dst, int64_t n,
                              hipStream_t stream);
 hipError_t launch_cache_free(const xq_kv& kv, int32_t* refs, int32_t* tables, int64_t slots,

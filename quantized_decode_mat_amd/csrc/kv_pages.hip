@@ -34,6 +34,9 @@ struct PageArgs {
   int64_t whole;                              // bytes of a page of one layer, when it is one run; else 0
   int layers, kv_heads, page_tokens, pages;
   int pieces;                                 // workgroups that share a page of one layer
+  int exp_words;                              // of 4 bits: dwords of a row's exponents; else 0
+  uint8_t* exp_base[2];
+  int64_t exp_layer[2], exp_page[2], exp_head[2], exp_tok[2];  // bytes
 };
 
 // One page of one layer of k or v, or a part of it: 16-byte words.
@@ -64,6 +67,18 @@ __device__ __forceinline__ void copy_page(const PageArgs& a, int which, int laye
       const int64_t at = (row / a.page_tokens) * a.head[which] + (row % a.page_tokens) * a.tok[which] +
                          (i - row * row_words) * 16;
       *reinterpret_cast<u32x4*>(dst + at) = *reinterpret_cast<const u32x4*>(src + at);
+    }
+  }
+  if (a.exp_words) {
+    const uint8_t* es = a.exp_base[which] + layer * a.exp_layer[which] + from * a.exp_page[which];
+    uint8_t* ed = a.exp_base[which] + layer * a.exp_layer[which] + to * a.exp_page[which];
+    const int64_t words = static_cast<int64_t>(a.kv_heads) * a.page_tokens * a.exp_words;
+    for (int64_t i = static_cast<int64_t>(piece) * kThreads + threadIdx.x; i < words;
+         i += static_cast<int64_t>(kThreads) * a.pieces) {
+      const int64_t row = i / a.exp_words;
+      const int64_t at = (row / a.page_tokens) * a.exp_head[which] + (row % a.page_tokens) * a.exp_tok[which] +
+                         (i - row * a.exp_words) * 4;
+      *reinterpret_cast<uint32_t*>(ed + at) = *reinterpret_cast<const uint32_t*>(es + at);
     }
   }
 }
@@ -510,21 +525,34 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(TableArgs a, PageArgs
 
 PageArgs page_args(const xq_kv& kv) {
   PageArgs a;
-  const int eb = elem_bytes(kv.dtype);
+  auto bytes_of = [&](int64_t n) { return cache_bytes(n, kv.dtype); };
   a.base[0] = static_cast<uint8_t*>(kv.k);
   a.base[1] = static_cast<uint8_t*>(kv.v);
   const int64_t* strides[2] = {kv.k_stride, kv.v_stride};
-  a.rows_bytes = kv.dim * eb;
+  a.rows_bytes = bytes_of(kv.dim);
   a.whole = kv.kv_heads * kv.page * a.rows_bytes;
   for (int i = 0; i < 2; ++i) {
-    a.layer[i] = strides[i][0] * eb;
-    a.page[i] = strides[i][1] * eb;
-    a.head[i] = strides[i][2] * eb;
-    a.tok[i] = strides[i][3] * eb;
+    a.layer[i] = bytes_of(strides[i][0]);
+    a.page[i] = bytes_of(strides[i][1]);
+    a.head[i] = bytes_of(strides[i][2]);
+    a.tok[i] = bytes_of(strides[i][3]);
     const int64_t h = strides[i][2], t = strides[i][3];
     const bool by_head = (t == kv.dim || kv.page == 1) && (h == kv.page * kv.dim || kv.kv_heads == 1);
     const bool by_token = (h == kv.dim || kv.kv_heads == 1) && (t == kv.kv_heads * kv.dim || kv.page == 1);
     if (!by_head && !by_token) a.whole = 0;
+  }
+  a.exp_words = 0;
+  if (kv.dtype == XQ_E2M1) {
+    a.exp_words = static_cast<int>(exp_row_bytes(kv.dim) / 4);
+    a.exp_base[0] = static_cast<uint8_t*>(kv.k_exp);
+    a.exp_base[1] = static_cast<uint8_t*>(kv.v_exp);
+    const int64_t* es[2] = {kv.k_exp_stride, kv.v_exp_stride};
+    for (int i = 0; i < 2; ++i) {
+      a.exp_layer[i] = es[i][0];
+      a.exp_page[i] = es[i][1];
+      a.exp_head[i] = es[i][2];
+      a.exp_tok[i] = es[i][3];
+    }
   }
   a.layers = static_cast<int>(kv.layers);
   a.kv_heads = static_cast<int>(kv.kv_heads);

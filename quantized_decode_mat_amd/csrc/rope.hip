@@ -20,6 +20,7 @@
 
 #include "kv_device.h"
 #include "kv_launch.h"
+#include "kv_view.h"
 
 namespace xq {
 namespace {
@@ -42,6 +43,8 @@ struct RopeArgs {
   int bound[3];                      // first pair of axes 1, 2 and 3
   FastDiv items;                     // dim / 8, pieces of a head
   float k_scale, v_scale;
+  ExpView exps;
+  FastDiv quarters;                  // dim / 4
 };
 
 __device__ __forceinline__ void sin_cos(double angle, float* s, float* c) {
@@ -197,6 +200,186 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
   }
 }
 
+// Sine and cosine in f64: the same reduction (2^-105 of pi/2 is left out), then
+// Taylor sums whose first left-out terms are below 2^-60.
+__device__ __forceinline__ void sin_cos(double angle, double* s, double* c) {
+  const double n = rint(angle * 0.63661977236758134308);
+  double x = fma(n, -1.57079632679489655800, angle);
+  x = fma(n, -6.12323399573676603587e-17, x);
+  const double y = x * x;
+  double sn = 1.0 / 355687428096000.0;
+  sn = fma(sn, y, -1.0 / 1307674368000.0);
+  sn = fma(sn, y, 1.0 / 6227020800.0);
+  sn = fma(sn, y, -1.0 / 39916800.0);
+  sn = fma(sn, y, 1.0 / 362880.0);
+  sn = fma(sn, y, -1.0 / 5040.0);
+  sn = fma(sn, y, 1.0 / 120.0);
+  sn = fma(sn, y, -1.0 / 6.0);
+  sn = fma(sn * y, x, x);
+  double cs = -1.0 / 6402373705728000.0;
+  cs = fma(cs, y, 1.0 / 20922789888000.0);
+  cs = fma(cs, y, -1.0 / 87178291200.0);
+  cs = fma(cs, y, 1.0 / 479001600.0);
+  cs = fma(cs, y, -1.0 / 3628800.0);
+  cs = fma(cs, y, 1.0 / 40320.0);
+  cs = fma(cs, y, -1.0 / 720.0);
+  cs = fma(cs, y, 1.0 / 24.0);
+  cs = fma(cs, y, -0.5);
+  cs = fma(cs, y, 1.0);
+  const int q = static_cast<int>(n - 4.0 * floor(n * 0.25));
+  const double u = q & 1 ? cs : sn, w = q & 1 ? sn : cs;
+  *s = q & 2 ? -u : u;
+  *c = (q + 1) & 2 ? -w : w;
+}
+
+// The largest over each aligned group of 8 lanes.
+__device__ __forceinline__ int lane8_max(int v) {
+  v = max(v, dpp<kDppQuadSwap1>(v));
+  v = max(v, dpp<kDppQuadSwap2>(v));
+  return max(v, dpp<kDppRowHalfMirror>(v));
+}
+
+// The append to a cache of 4 bits. A thread takes four elements of k or v (or
+// eight of q), 8 threads next to each other a block of 32, whose power of two
+// they agree on. A code depends on the side of a border that its value lies
+// on, so k is turned, and k and v divided, in f64: the codes are those of the
+// exact values, up to a value within 2^-50 of a border. (A partner element is
+// loaded by both threads that need it; the second load is a cache hit.)
+template <bool VEC>
+__global__ __launch_bounds__(kThreads) void rope_append4_kernel(RopeArgs a) {
+  extern __shared__ double trig64[];  // [token][half] cosines, then sines
+  const int tid = threadIdx.x;
+  const int t0 = (blockIdx.x / a.head_blocks) * a.per_block, hb = blockIdx.x % a.head_blocks;
+  const int tokens = min(a.per_block, a.tokens - t0);
+  double* sines = trig64 + a.per_block * a.half;
+  for (int i = tid; i < tokens * a.half; i += kThreads) {
+    const int t = i / a.half, pair = i - t * a.half;
+    const int axis = (pair >= a.bound[0]) + (pair >= a.bound[1]) + (pair >= a.bound[2]);
+    sin_cos(a.pos[axis * a.pos_stride + t0 + t] * a.freq[pair], &sines[i], &trig64[i]);
+  }
+  __syncthreads();
+
+  const int all = a.heads + 2 * a.kv_heads;
+  const int h0 = static_cast<int>(static_cast<int64_t>(all) * hb / a.head_blocks);
+  const int h1 = static_cast<int>(static_cast<int64_t>(all) * (hb + 1) / a.head_blocks);
+  // q, as in rope_kernel.
+  const int q_heads = max(0, min(h1, a.heads) - h0);
+  const int per_token = q_heads * static_cast<int>(a.items.d);
+  for (int i = tid; i < tokens * per_token; i += kThreads) {
+    const int t = i / per_token, j = i - t * per_token;
+    const int hi = div_by(j, a.items);
+    const int piece = j - hi * a.items.d;
+    const int64_t token = t0 + t;
+    const uint8_t* src = a.src[0] + token * a.row[0] + (h0 + hi) * a.head[0];
+    uint8_t* dst = a.out + token * a.out_row + (h0 + hi) * a.out_head;
+    const bool turns = piece * 4 < a.half, split = turns && !a.adjacent;
+    const int at0 = split ? piece * 4 : piece * 8, at1 = split ? a.half + piece * 4 : piece * 8 + 4;
+    f32x4 x = load4<VEC>(src, a.x_type, at0), y = load4<VEC>(src, a.x_type, at1);
+    if (turns) {
+      float c[4], s[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[e] = static_cast<float>(trig64[t * a.half + piece * 4 + e]);
+        s[e] = static_cast<float>(sines[t * a.half + piece * 4 + e]);
+      }
+      const f32x4 u = x, w = y;
+      if (split) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = u[e] * c[e] - w[e] * s[e];
+          y[e] = u[e] * s[e] + w[e] * c[e];
+        }
+      } else {
+        x = f32x4{u.x * c[0] - u.y * s[0], u.x * s[0] + u.y * c[0],
+                  u.z * c[1] - u.w * s[1], u.z * s[1] + u.w * c[1]};
+        y = f32x4{w.x * c[2] - w.y * s[2], w.x * s[2] + w.y * c[2],
+                  w.z * c[3] - w.w * s[3], w.z * s[3] + w.w * c[3]};
+      }
+    }
+    store4<VEC>(dst, a.out_type, at0, x);
+    store4<VEC>(dst, a.out_type, at1, y);
+  }
+
+  // k and v. 8 | dim / 4, so the 8 threads of a block are in one wave's row
+  // and take every turn of the loop together.
+  const int kv0 = max(0, h0 - a.heads), kv_here = max(0, h1 - a.heads) - kv0;
+  const int quarters = a.quarters.d, per = kv_here * quarters;
+  for (int i = tid; i < tokens * per; i += kThreads) {
+    const int t = i / per, j = i - t * per;
+    const int hi = div_by(j, a.quarters), at = (j - hi * quarters) * 4;
+    const bool is_v = kv0 + hi >= a.kv_heads;
+    const int head = kv0 + hi - (is_v ? a.kv_heads : 0);
+    const int64_t token = t0 + t;
+    const int64_t slot = a.slots[token];
+    if (slot < 0 || slot >= a.cache_slots) continue;
+    const uint8_t* src = is_v ? a.src[2] + token * a.row[2] + head * a.head[2]
+                              : a.src[1] + token * a.row[1] + head * a.head[1];
+    const f32x4 own = load4<VEC>(src, a.x_type, at);
+    double x[4] = {own.x, own.y, own.z, own.w};
+    if (!is_v && at < 2 * a.half) {
+      const double* c = trig64 + t * a.half;
+      const double* s = sines + t * a.half;
+      if (a.adjacent) {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const int pair = (at + e) / 2;
+          const double u = x[e], w = x[e + 1];
+          x[e] = u * c[pair] - w * s[pair];
+          x[e + 1] = u * s[pair] + w * c[pair];
+        }
+      } else {
+        // The second half's elements turn by the sine as they are, the first
+        // half's by its negative.
+        const bool second = at >= a.half;
+        const int first = second ? at - a.half : at;
+        const f32x4 other = load4<VEC>(src, a.x_type, second ? first : at + a.half);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const double turn = s[first + e] * static_cast<double>(other[e]);
+          x[e] = x[e] * c[first + e] + (second ? turn : -turn);
+        }
+      }
+    }
+    const float scale = is_v ? a.v_scale : a.k_scale;
+    if (scale != 1.f) {
+      // The quotient with one correction: where x / scale is a number of f64,
+      // a border between two codes say, that number.
+      const double d = scale, r = 1.0 / d;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const double q = x[e] * r, rest = fma(-q, d, x[e]);
+        x[e] = fabs(q) < INFINITY ? copysign(fma(rest, r, q), q) : q;  // (-0 + 0 would be 0)
+      }
+    }
+    // The largest |x| by its upper word: m * 2^E is below 7 * 2^e from e = E - 2
+    // on where m < 1.75, else from E - 1 on.
+    int top = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, static_cast<int>(__double2hiint(x[e]) & 0x7fffffff));
+    top = lane8_max(top);
+    const bool nan = top > 0x7ff00000;
+    const int power = min(max((top >> 20) - 1023 - 2 + ((top >> 18 & 3) == 3), -23), 13);
+    const double down = __hiloint2double((1023 - power) << 20, 0);
+    uint32_t codes = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const double u = fabs(x[e]) * down;
+      const uint32_t code = (u > 0.25) + (u >= 0.75) + (u > 1.25) + (u >= 1.75) + (u > 2.5) + (u >= 3.5) + (u > 5.0);
+      codes |= (code | (__double2hiint(x[e]) < 0 ? 8u : 0u)) << (4 * e);
+    }
+    const uint32_t page = div_by(static_cast<uint32_t>(slot), a.kv.page);
+    const int64_t in = slot - static_cast<int64_t>(page) * a.kv.page.d;
+    uint8_t* row = is_v ? a.kv.v + page * a.kv.v_page + head * a.kv.v_head + in * a.kv.v_tok
+                        : a.kv.k + page * a.kv.k_page + head * a.kv.k_head + in * a.kv.k_tok;
+    *reinterpret_cast<uint16_t*>(row + at / 2) = static_cast<uint16_t>(codes);
+    if (at % 32 == 0) {
+      uint8_t* exps = is_v ? a.exps.v + page * a.exps.v_page + head * a.exps.v_head + in * a.exps.v_tok
+                           : a.exps.k + page * a.exps.k_page + head * a.exps.k_head + in * a.exps.k_tok;
+      exps[at / 32] = static_cast<uint8_t>(nan ? 255 : power + 127);
+    }
+  }
+}
+
 // Whether four elements at a multiple of four into any row are one aligned
 // word.
 bool rows_aligned(const RowsView& r) {
@@ -229,11 +412,8 @@ hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k
       a.head[1 + i] = kvs[i]->head * xb;
       vec = vec && rows_aligned(*kvs[i]);
     }
-    const int eb = elem_bytes(kv->dtype);
-    a.kv = KvView{static_cast<uint8_t*>(kv->k), static_cast<uint8_t*>(kv->v),
-                  kv->k_stride[1] * eb, kv->k_stride[2] * eb, kv->k_stride[3] * eb,
-                  kv->v_stride[1] * eb, kv->v_stride[2] * eb, kv->v_stride[3] * eb,
-                  fast_div(static_cast<uint32_t>(kv->page)), static_cast<int>(kv->pages)};
+    a.kv = kv_view(*kv);
+    a.exps = exp_view(*kv);
     a.kv_heads = static_cast<int>(kv->kv_heads);
     a.cache_type = kv->dtype;
     a.cache_slots = kv->pages * kv->page;
@@ -256,6 +436,8 @@ hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k
     a.bound[i] = i + 1 < rope.axes ? first : a.half;
   }
   a.items = fast_div(static_cast<uint32_t>(dim / 8));
+  a.quarters = fast_div(static_cast<uint32_t>(dim / 4));
+  const bool four = kv && kv->dtype == kE2M1;
   // One token a workgroup, its heads shared between several where tokens are
   // few. More tokens only where a token's items leave more than a quarter of
   // the threads without work and there are tokens enough: 8192 tokens of 64
@@ -269,7 +451,7 @@ hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k
     ++a.per_block;
   const int64_t blocks = (tokens + a.per_block - 1) / a.per_block;
   a.head_blocks = static_cast<int>(std::clamp<int64_t>(1024 / blocks, 1, (items + kThreads - 1) / kThreads));
-  const size_t lds = static_cast<size_t>(a.per_block) * a.half * 2 * sizeof(float);
+  const size_t lds = static_cast<size_t>(a.per_block) * a.half * 2 * (four ? sizeof(double) : sizeof(float));
   // A launch's threads are counted in 32 bits, and more wrap round without an
   // error: so many workgroups (of 2^24 - 1) take the tokens in several launches.
   const int64_t most = int64_t{1} << 23;
@@ -277,7 +459,11 @@ hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k
     const int64_t now = std::min(left, most), done = now * a.per_block;
     a.tokens = static_cast<int>(std::min(done, tokens));
     const dim3 grid(static_cast<uint32_t>(now * a.head_blocks));
-    if (vec)
+    if (four && vec)
+      rope_append4_kernel<true><<<grid, dim3(kThreads), lds, stream>>>(a);
+    else if (four)
+      rope_append4_kernel<false><<<grid, dim3(kThreads), lds, stream>>>(a);
+    else if (vec)
       rope_kernel<true><<<grid, dim3(kThreads), lds, stream>>>(a);
     else
       rope_kernel<false><<<grid, dim3(kThreads), lds, stream>>>(a);

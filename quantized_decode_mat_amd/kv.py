@@ -17,7 +17,7 @@ import torch
 from . import _check as _raise
 from . import lib as _load
 
-XQ_F32, XQ_BF16, XQ_F16, XQ_E4M3 = range(4)
+XQ_F32, XQ_BF16, XQ_F16, XQ_E4M3, XQ_E2M1 = range(5)
 _L = None
 
 
@@ -46,7 +46,8 @@ def _workspace(ws, index: int):
 
 
 _ROW = {torch.float32: XQ_F32, torch.bfloat16: XQ_BF16, torch.float16: XQ_F16}
-_CACHE = {torch.bfloat16: XQ_BF16, torch.float16: XQ_F16, torch.float8_e4m3fn: XQ_E4M3}
+_CACHE = {torch.bfloat16: XQ_BF16, torch.float16: XQ_F16, torch.float8_e4m3fn: XQ_E4M3,
+          torch.float4_e2m1fn_x2: XQ_E2M1}
 
 
 class _KV(ctypes.Structure):
@@ -54,7 +55,9 @@ class _KV(ctypes.Structure):
                 ("layers", ctypes.c_int64), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
                 ("page", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("k_stride", ctypes.c_int64 * 4), ("v_stride", ctypes.c_int64 * 4),
-                ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+                ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("k_exp_stride", ctypes.c_int64 * 4), ("v_exp_stride", ctypes.c_int64 * 4)]
 
 
 class _Rope(ctypes.Structure):
@@ -74,9 +77,14 @@ class xq_kv_cache:
     [layers, pages, kv_heads, page, dim], bfloat16, float16 or float8_e4m3fn,
     any strides with contiguous dims (a pool stored [pages, page, kv_heads,
     dim] is passed transposed). What is stored stands for k * k_scale and
-    v * v_scale."""
+    v * v_scale.
 
-    def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0):
+    A cache of 4 bits is float4_e2m1fn_x2, whose last dim holds dim / 2 bytes,
+    with ``k_exp`` and ``v_exp``, float8_e8m0fnu of the same leading shape: the
+    powers of two of the rows' blocks of 32 dims, dim / 32 of them in rows of 4
+    (dims up to 128) or 8."""
+
+    def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0, k_exp=None, v_exp=None):
         for t, what in ((k, "k"), (v, "v")):
             _device(t, what)
             if t.dim() not in (4, 5):
@@ -90,21 +98,39 @@ class xq_kv_cache:
             raise ValueError("k and v differ in shape, type or device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
         shape = tuple(k.shape) if k.dim() == 5 else (1, *k.shape)
-        self.layers, self.pages, self.kv_heads, self.page, self.dim = shape
         self.index = k.device.index
+        four = k.dtype == torch.float4_e2m1fn_x2
+        if four:
+            shape = (*shape[:4], 2 * shape[4])
+        self.layers, self.pages, self.kv_heads, self.page, self.dim = shape
+        for t, what in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+            if not four and t is not None:
+                raise ValueError("%s: a cache of %s has no exponents" % (what, k.dtype))
+            if four:
+                _device(t, what)
+                if (t.dtype != torch.float8_e8m0fnu or t.device != k.device or t.stride(-1) != 1
+                        or tuple(t.shape) != (*k.shape[:-1], 4 if self.dim <= 128 else 8)):
+                    raise ValueError("%s: expected float8_e8m0fnu %s with contiguous rows, on the cache's device"
+                                     % (what, [*k.shape[:-1], 4 if self.dim <= 128 else 8]))
+        self.k_exp, self.v_exp = k_exp, v_exp
         # a dim of size 1 has no stride that matters
-        def strides(t):
+        def strides(t, unit=1):
             s = t.stride() if t.dim() == 5 else (0, *t.stride())
-            return (ctypes.c_int64 * 4)(*(0 if n == 1 else x for n, x in zip(shape[:4], s)))
-        self._c = _KV(k.data_ptr(), v.data_ptr(), *shape, strides(k), strides(v), _CACHE[k.dtype],
+            return (ctypes.c_int64 * 4)(*(0 if n == 1 else x * unit for n, x in zip(shape[:4], s)))
+        unit = 2 if four else 1
+        self._c = _KV(k.data_ptr(), v.data_ptr(), *shape, strides(k, unit), strides(v, unit), _CACHE[k.dtype],
                       self.k_scale, self.v_scale)
+        if four:
+            self._c.k_exp, self._c.v_exp = k_exp.data_ptr(), v_exp.data_ptr()
+            self._c.k_exp_stride, self._c.v_exp_stride = strides(k_exp), strides(v_exp)
         self._ref = ctypes.byref(self._c)
 
     def layer(self, i: int) -> "xq_kv_cache":
         """One layer, for the calls that take one (attention, the append)."""
         if self.k.dim() == 4:
             raise ValueError("this cache has one layer")
-        return xq_kv_cache(self.k[i], self.v[i], self.k_scale, self.v_scale)
+        exps = {} if self.k_exp is None else dict(k_exp=self.k_exp[i], v_exp=self.v_exp[i])
+        return xq_kv_cache(self.k[i], self.v[i], self.k_scale, self.v_scale, **exps)
 
 
 class xq_rope_plan:
@@ -273,6 +299,22 @@ def xq_rope_append(q_out, kv: xq_kv_cache, q, k, v, pos, rope: xq_rope_plan, slo
                                 _ints(slots, "slots", index, tokens, torch.int64),
                                 _raw_stream(stream, index)),
            "xq_rope_append")
+
+
+def xq_cache_read(k_out, v_out, kv: xq_kv_cache, slots, stream=None) -> None:
+    """The tokens at ``slots`` as values, [tokens, kv_heads, dim] each."""
+    index = kv.index
+    kp, kind, k_row, k_head = _rows(k_out, "k_out", index)
+    vp, v_kind, v_row, v_head = _rows(v_out, "v_out", index)
+    tokens = slots.numel()
+    if v_kind != kind:
+        raise ValueError("k_out and v_out differ in type")
+    if not tuple(k_out.shape) == tuple(v_out.shape) == (tokens, kv.kv_heads, kv.dim):
+        raise ValueError("k_out and v_out: expected [%d, %d, %d]" % (tokens, kv.kv_heads, kv.dim))
+    _check(lib().xq_cache_read(kp, k_row, k_head, vp, v_row, v_head, kind, kv._ref,
+                               _ints(slots, "slots", index, tokens, torch.int64), tokens,
+                               _raw_stream(stream, index)),
+           "xq_cache_read")
 
 
 def xq_cache_workspace_bytes(pages: int, slots: int) -> int:
