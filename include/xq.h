@@ -12,11 +12,12 @@
  *    ("cajeta.xpu — one kernel, any device", section 2.2: buffers are the
  *    caller's allocations). The library allocates no memory and keeps no
  *    per-call state; it never synchronizes a stream or the device.
- *  - Six entry points need device scratch beyond their inputs and outputs
+ *  - Eight entry points need device scratch beyond their inputs and outputs
  *    (xq_gemm_q4k_small_m's split-K partials and arrival counters,
  *    xq_gemv_q4k_q8k's arrival counters, xq_gemm_q4k_id's expert map,
  *    xq_attn_decode's split partials and arrival counters, the lists of
- *    xq_cache_fork and xq_cache_compact). The
+ *    xq_cache_fork and xq_cache_compact, the logits of xq_moe_route, the hidden
+ *    values of xq_moe_q4k). The
  *    caller passes it as `workspace` (device memory, 256-byte aligned) and
  *    `workspace_bytes`; the matching *_workspace_bytes query gives the exact
  *    bytes a call needs (0: none, and then workspace may be NULL). The caller
@@ -588,6 +589,67 @@ xq_status xq_cache_compact(const xq_kv *kv, int32_t *refs, int32_t *tables, int6
                            int64_t width, int64_t stride, int32_t *status, void *workspace,
                            size_t workspace_bytes, void *stream);
 size_t xq_cache_workspace_bytes(int64_t pages, int64_t slots);
+
+/* ---- A mixture-of-experts layer for a few tokens ---- */
+
+/* Scores of the experts, from their logits. */
+enum { XQ_SOFTMAX = 0, XQ_SIGMOID = 1 };
+
+/*
+ * The router: for each token the `used` experts of the highest scores, the
+ * highest first, and their weights.
+ *   logit[e] = router[e] . x[t] (f32 sums);
+ *   score[e] = exp(logit[e]) / sum over all experts, or 1 / (1 + exp(-logit[e]));
+ *   ids[t] = those with the largest score[e] + bias[e] (bias may be NULL), the
+ *     lowest index among equals, NaN below everything;
+ *   weights[t][k] = score[ids[t][k]] (bias not in it), divided by the sum over
+ *     the chosen where normalize = 1 (0 where that sum is 0), times scale.
+ *  x       device [tokens][K] of type x_type (XQ_F32, XQ_BF16, XQ_F16), rows
+ *          x_row elements apart; router device [experts][K] of type router_type
+ *          (the same three), contiguous. Both bases and x's rows 16-byte aligned.
+ *  bias    device f32[experts] or NULL; ids device int32[tokens][used], weights
+ *          device f32[tokens][used]. 4-byte aligned.
+ *  1 <= tokens <= 512; 1 <= used <= 64, used <= experts <= 1024; K a multiple of
+ *  8, 8..XQ_MAX_K. scale finite.
+ *  workspace  arrival counters in its first 96 KiB, then the logits:
+ *          xq_moe_route_workspace_bytes(tokens, experts) bytes, zeroed before
+ *          first use.
+ * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
+ */
+xq_status xq_moe_route(int32_t *ids, float *weights, const void *x, int32_t x_type, int64_t x_row,
+                       const void *router, int32_t router_type, const float *bias, int64_t tokens,
+                       int64_t experts, int64_t used, int64_t K, int32_t score, int32_t normalize,
+                       float scale, void *workspace, size_t workspace_bytes, void *stream);
+size_t xq_moe_route_workspace_bytes(int64_t tokens, int64_t experts);  /* 0 if the sizes are refused */
+
+/*
+ * The chosen experts' feed-forward on Q4_K weights, and its weighted sum:
+ *   h[t][k] = silu(G_e x^[t]) * (U_e x^[t]), e = ids[t][k], silu(g) = g / (1 + exp(-g)),
+ *   y[t] = sum_k weights[t][k] * (D_e h^[t][k]),
+ * where x^ and h^ are x[t] and h[t][k] in q8_K (as xq_quantize_q8k, but with
+ * d = amax * (1/127), one f32 product with the constant as f32 rounds it) and
+ * the products are xq_gemv_q4k's; h is f32, the sum over k in f32, one rounding
+ * to y's type. A slot whose id lies outside 0..experts-1 is left out (a token
+ * with no other gets zeros); an id may stand in several slots of a token.
+ * x is to be finite, as for xq_quantize_q8k.
+ *  y, x    device [tokens][hidden] of type io (XQ_F32, XQ_BF16, XQ_F16), rows
+ *          y_row and x_row elements apart; x and its rows 16-byte aligned, y
+ *          aligned to its elements.
+ *  gate, up  device Q4_K, `experts` experts of ffn rows of hidden columns back to
+ *          back; down the same of hidden rows of ffn columns. 16-byte aligned.
+ *  ids     device int32[tokens][used], weights device f32[tokens][used].
+ *  tokens, used >= 1, tokens * used <= 512 (more are xq_gemm_q4k_id's); 1 <=
+ *  experts <= 1024; hidden and ffn multiples of 256, 256..32768.
+ *  workspace  h, and for several tokens the q8_K rows and the slots' results,
+ *          behind the first 96 KiB: xq_moe_q4k_workspace_bytes(...) bytes.
+ * Errors: XQ_E_NULL, XQ_E_SHAPE, XQ_E_ALIGN, XQ_E_DEVICE, XQ_E_LAUNCH.
+ */
+xq_status xq_moe_q4k(void *y, int64_t y_row, const void *x, int64_t x_row, int32_t io,
+                     const void *gate, const void *up, const void *down, const int32_t *ids,
+                     const float *weights, int64_t tokens, int64_t used, int64_t experts,
+                     int64_t hidden, int64_t ffn, void *workspace, size_t workspace_bytes,
+                     void *stream);
+size_t xq_moe_q4k_workspace_bytes(int64_t tokens, int64_t used, int64_t hidden, int64_t ffn);  /* 0 if refused */
 
 /*
  * Measurement helper, not part of the method: read `bytes` of device memory

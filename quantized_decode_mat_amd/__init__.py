@@ -106,6 +106,14 @@ def lib() -> ctypes.CDLL:
             L.xq_cache_workspace_bytes.argtypes = [I, I]
             for f in ("xq_attn_decode_workspace_bytes", "xq_cache_workspace_bytes"):
                 getattr(L, f).restype = Z
+            L.xq_moe_route.argtypes = [P, P, P, S, I, P, S, P, I, I, I, I, S, S, F, P, Z, P]
+            L.xq_moe_q4k.argtypes = [P, I, P, I, S, P, P, P, P, P, I, I, I, I, I, P, Z, P]
+            L.xq_moe_route_workspace_bytes.argtypes = [I, I]
+            L.xq_moe_q4k_workspace_bytes.argtypes = [I, I, I, I]
+            for f in ("xq_moe_route", "xq_moe_q4k"):
+                getattr(L, f).restype = S
+            for f in ("xq_moe_route_workspace_bytes", "xq_moe_q4k_workspace_bytes"):
+                getattr(L, f).restype = Z
             L.xq_status_name.argtypes = [S]
             L.xq_status_name.restype = ctypes.c_char_p
             L.xq_last_error.argtypes = []
@@ -305,3 +313,5 @@ from .kv import (  # noqa: E402  (they use the helpers above)
     XQ_BF16, XQ_E2M1, XQ_E4M3, XQ_F16, XQ_F32, xq_attn_decode, xq_attn_decode_workspace_bytes,
     xq_attn_prefill, xq_cache_compact, xq_cache_copy, xq_cache_fork, xq_cache_free, xq_cache_read,
     xq_cache_workspace_bytes, xq_kv_cache, xq_rope, xq_rope_append, xq_rope_plan)
+from .moe import (  # noqa: E402
+    XQ_SIGMOID, XQ_SOFTMAX, xq_moe_q4k, xq_moe_q4k_workspace_bytes, xq_moe_route, xq_moe_route_workspace_bytes)

@@ -43,8 +43,10 @@ SOURCES = [
     "rope.hip",
     "kv_pages.hip",
     "kv_read.hip",
+    "moe.hip",
     "xq_api.cpp",
     "kv_api.cpp",
+    "moe_api.cpp",
 ]
 
 FLAGS = [

@@ -27,10 +27,14 @@ struct Q8KLane {
   float d;
 };
 
+// PRODUCT: the scale is amax times 1/127 as f32 rounds it, where a workgroup
+// quantizes what it needs for itself (a division less; in 1 of 25 blocks the
+// scale's last bit is another).
+template <bool PRODUCT = false>
 __device__ __forceinline__ Q8KLane q8k_block_lane(const float4 v) {
   const float a = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
   const float amax = wave_max(a);
-  const float d = amax / 127.0f;
+  const float d = PRODUCT ? amax * (1.0f / 127.0f) : amax / 127.0f;
 
   int q0 = 0, q1 = 0, q2 = 0, q3 = 0;
   if (d != 0.0f) {
@@ -49,8 +53,9 @@ __device__ __forceinline__ Q8KLane q8k_block_lane(const float4 v) {
 }
 
 // Writes the whole 320-byte block at `out` (global memory or LDS).
+template <bool PRODUCT = false>
 __device__ __forceinline__ void q8k_block_wave(const float4 v, uint8_t* out, int lane) {
-  const Q8KLane o = q8k_block_lane(v);
+  const Q8KLane o = q8k_block_lane<PRODUCT>(v);
   reinterpret_cast<uint32_t*>(out)[lane] = o.packed;
   if ((lane & 7) == 0) reinterpret_cast<int32_t*>(out + 256)[lane >> 3] = o.sum;
   if (lane == 0) *reinterpret_cast<float*>(out + 288) = o.d;
