@@ -416,7 +416,7 @@ typedef struct {
  *           pages per row; lens device int32[seqs].
  *  heads a multiple of kv_heads, heads / kv_heads <= 256, seqs * kv_heads <= 2^20,
  *  seqs * kv_heads * ceil(heads / kv_heads / 16) < 2^24;
- *  k, and v, of one layer within 64 GiB.
+ *  k, and v, of one layer within 64 GiB, their exponents within 16.
  *  scale finite, and scale * k_scale * log2(e) too.
  *  window in 0..2^30 (0: none), sinks in 0..2^30 (read only with a window).
  *  max_len in 1..2^30: no length is above it (longer ones are clamped); the split of

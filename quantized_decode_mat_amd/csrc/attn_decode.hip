@@ -38,6 +38,7 @@
 // many pieces as f32 has bits (three of bf16's 8, two of f16's 11). The
 // instructions wait on memory, so the pieces cost no time.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kv_device.h"
@@ -77,7 +78,11 @@ struct DecodeArgs {
   FastDiv ranges;  // parts that the sequences' steps are shared out to
   float c;        // scale * k_scale * log2(e)
   float v_scale;
+  // Of 4 bits: the exponents, strides in dwords; c is |c| there, and `flip` says
+  // that q's sign is turned, `zero` that q counts as 0 (c is then 1).
   ExpView exps;
+  uint32_t ke_page, ke_tok, ve_page, ve_tok;
+  int flip, zero;
 };
 
 // Sum and maximum over the four lanes that hold one head.
@@ -88,6 +93,18 @@ __device__ __forceinline__ float heads_max(float v) {
 __device__ __forceinline__ float heads_sum(float v) {
   v += __shfl_xor(v, 16, kWave);
   return v + __shfl_xor(v, 32, kWave);
+}
+
+// The same maximum without LDS: rows of 16 lanes change places.
+__device__ __forceinline__ float swapped_max(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t a0 = a[0], a1 = a[1];
+  const float x = fmaxf(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+  const uint32_t w = __builtin_bit_cast(uint32_t, x);
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  const uint32_t b0 = b[0], b1 = b[1];
+  return fmaxf(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
 }
 
 // A wave's lanes see what they have left for each other in LDS. (No
@@ -154,8 +171,8 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   constexpr int OS = DP + 4;                       // floats of a joined row in LDS
   extern __shared__ float lds[];
   __shared__ __attribute__((aligned(16))) uint32_t places[kWaves][2][kTile];
-  // Exponents of a tile's rows of k and of v.
-  __shared__ __attribute__((aligned(16))) uint32_t powers[F4 ? kWaves : 1][2][NE][kTile];
+  // Of 4 bits: the powers of two of a tile's rows of k and of v.
+  __shared__ __attribute__((aligned(16))) float powers[F4 ? kWaves : 1][2][DP / 32][kTile];
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int l16 = lane % 16, lg = lane / 16;
@@ -175,7 +192,10 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   // which begins at `seq0`. Workgroups next to each other have one part and the
   // sequence's units: they walk over the same pages at the same time, and a
   // page's heads, which are neighbours in memory, are read together.
-  const int unit = blockIdx.x % per_seq, range = blockIdx.x / per_seq;
+  // (Of 4 bits, whose rows may be less than a cache line: on one XCD, whose L2
+  // then reads the line once. Blocks go to the eight XCDs in turn.)
+  const int block = F4 && gridDim.x % 8 == 0 ? blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8 : blockIdx.x;
+  const int unit = block % per_seq, range = block / per_seq;
   int seq, n, steps, at, stop, seq0, each;
   if (a.shared) {
     // Every wave adds up the sequences' steps for itself, 64 sequences at a
@@ -278,9 +298,12 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   // need those of tokens l % 16 and 16 + l % 16, its V loads those of 4g .. 4g+3
   // and 16 + those.
   auto token_of = [&](int u) { return u < ns ? u : lo + (u - ns); };
+  uint32_t next_slot = 0;  // of 4 bits: the place in its page of the token last looked up
   auto page_of = [&](int u0) {
     const int u = u0 + lane % kTile;
-    const int page = table[u < end ? div_by(token_of(u), a.kv.page) : 0];
+    const uint32_t j = token_of(u), at = div_by(j, a.kv.page);
+    if constexpr (F4) next_slot = j - at * a.kv.page.d;
+    const int page = table[u < end ? at : 0];
     return u < end ? page : -1;
   };
   uint32_t live;  // bit t: token t of the tile is there
@@ -288,30 +311,29 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   // Of 4 bits: lanes 0..31 read the exponents of k for the tile's tokens, the
   // others those of v.
   const uint8_t* eb = nullptr;
-  const uint8_t* e_at = nullptr;
+  uint32_t e_at = 0, e_page = 0, e_tok = 0;
   if constexpr (F4) {
     eb = lane < kTile ? a.exps.k + kvh * a.exps.k_head : a.exps.v + kvh * a.exps.v_head;
-    e_at = eb;
+    e_page = lane < kTile ? a.ke_page : a.ve_page;
+    e_tok = lane < kTile ? a.ke_tok : a.ve_tok;
   }
   auto place = [&](int u0, int page) {
     const int u = u0 + lane % kTile;
     const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.kv.pages);
     const uint32_t j = token_of(u);
-    const uint32_t slot = j - div_by(j, a.kv.page) * a.kv.page.d;
+    const uint32_t slot = F4 ? next_slot : j - div_by(j, a.kv.page) * a.kv.page.d;
     // A token that is not there reads what was read last in its stead, at
     // first the start of page 0, which is always there; its score is hidden
     // and its v is cleared.
     k_at = ok ? page * a.k_page16 + slot * a.k_tok16 : k_at;
     v_at = ok ? page * a.v_page16 + slot * a.v_tok16 : v_at;
-    if constexpr (F4)
-      e_at = ok ? eb + page * (lane < kTile ? a.exps.k_page : a.exps.v_page) +
-                      slot * (lane < kTile ? a.exps.k_tok : a.exps.v_tok)
-                : e_at;
+    if constexpr (F4) e_at = ok ? page * e_page + slot * e_tok : e_at;
     lanes_meet();
     places[wave][0][lane % kTile] = k_at;
     places[wave][1][lane % kTile] = v_at;
     lanes_meet();
     live = static_cast<uint32_t>(__ballot(ok));
+    if constexpr (F4) live = __builtin_amdgcn_readfirstlane(live);
   };
   u32x4 kr[2][KN];
   std::conditional_t<F4, uint32_t, u32x4> vr[VC][8];
@@ -340,7 +362,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     }
     if constexpr (F4) {
 #pragma unroll
-      for (int i = 0; i < NE; ++i) er[i] = reinterpret_cast<const uint32_t*>(e_at)[i];
+      for (int i = 0; i < NE; ++i) er[i] = reinterpret_cast<const uint32_t*>(eb + static_cast<uint64_t>(e_at) * 4)[i];
     }
   };
   auto load_v = [&]() {
@@ -398,7 +420,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     u32x4 raw[QS][IB / 2];
 #pragma unroll
     for (int s = 0; s < QS; ++s) {
-      const bool in = l16 < heads && (FULL || q_dim(s) < a.dim);
+      const bool in = l16 < heads && (FULL || q_dim(s) < a.dim) && !(F4 && a.zero);
 #pragma unroll
       for (int i = 0; i < IB / 2; ++i) {
         raw[s][i] = load_words<16>(in ? qr + q_dim(s) * IB + i * 16 : a.q);
@@ -408,8 +430,12 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     // The first tile's loads go out behind q's, before q is waited for.
     if (u0 < end) {
       page = page_of(u0);
+      const uint32_t slot = next_slot;
       const int next = page_of(u0 + kStep);
+      const uint32_t after = next_slot;
+      next_slot = slot;
       place(u0, page);
+      next_slot = after;
       page = next;
       load_k();
       load_v();
@@ -443,6 +469,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         float u = x[s][e] * mul, w = x[s][e + 1] * mul;
+        if (F4 && a.flip) u = -u, w = -w;
 #pragma unroll
         for (int p = 0; p < NQ; ++p) {
           const uint32_t h = pack2<MT>(u, w);
@@ -461,27 +488,26 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     const uint32_t here = live;
     float kp[2][KN];  // of 4 bits: the powers of the lane's K
     if constexpr (F4) {
-      // The rows' exponents go through LDS to the lanes that hold their codes.
+      // The rows' powers go through LDS to the lanes that hold their codes.
       lanes_meet();
 #pragma unroll
-      for (int i = 0; i < NE; ++i) powers[wave][lane / kTile][i][lane % kTile] = er[i];
+      for (int b = 0; b < DP / 32; ++b)
+        powers[wave][lane / kTile][b][lane % kTile] = block_power((er[b / 4] >> (b % 4 * 8)) & 0xff);
       lanes_meet();
       constexpr int kBlocks = KL == 4 ? 1 : 2;  // K loads of a block
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int s = 0; s < KN; ++s) {
-          const int b = (s * 4 + lg) / kBlocks;
-          kp[t][s] = block_power((powers[wave][0][NE == 1 ? 0 : b / 4][t * 16 + l16] >> (b % 4 * 8)) & 0xff);
-        }
+        for (int s = 0; s < KN; ++s)
+          kp[t][s] = powers[wave][0][min((s * 4 + lg) / kBlocks, DP / 32 - 1)][t * 16 + l16];
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
         const int b = min((c * 16 + l16) * VE / 32, DP / 32 - 1);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const u32x4 e = *reinterpret_cast<const u32x4*>(&powers[wave][1][NE == 1 ? 0 : b / 4][t * 16 + lg * 4]);
+          const f32x4 e = *reinterpret_cast<const f32x4*>(&powers[wave][1][b][t * 16 + lg * 4]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vp[c][t * 4 + i] = block_power((e[i] >> (b % 4 * 8)) & 0xff);
+          for (int i = 0; i < 4; ++i) vp[c][t * 4 + i] = e[i];
         }
       }
     }
@@ -532,20 +558,34 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     }
     float s[8];
     float top = -INFINITY;
+    if constexpr (F4) {
+      // The scale is above 0: the largest score is the largest product's, and
+      // scaling and subtraction are one instruction. Most tiles hide nothing.
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s[i] = st[i / 4][i % 4] * qs;
-      if (!((sees >> ((i / 4) * 16 + lg * 4 + i % 4)) & 1)) s[i] = -INFINITY;
-      top = fmaxf(top, s[i]);
+      for (int i = 0; i < 8; ++i) s[i] = st[i / 4][i % 4];
+      if (CHUNK ? __ballot(sees != ~0u) != 0 : here != ~0u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = (sees >> ((i / 4) * 16 + lg * 4 + i % 4)) & 1 ? s[i] : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, s[i]);
+      top = fmaxf(m, swapped_max(top) * qs);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[i] = st[i / 4][i % 4] * qs;
+        if (!((sees >> ((i / 4) * 16 + lg * 4 + i % 4)) & 1)) s[i] = -INFINITY;
+        top = fmaxf(top, s[i]);
+      }
+      top = fmaxf(m, heads_max(top));
     }
-    top = fmaxf(m, heads_max(top));
     const float base = top == -INFINITY ? 0.f : top;
     const float alpha = exp2_fast(m - base);
     m = top;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      s[i] = exp2_fast(s[i] - base);
+      s[i] = F4 ? exp2_fast(fmaf(s[i], qs, -base)) : exp2_fast(s[i] - base);
       sum += s[i];
     }
     l = l * alpha + sum;
@@ -736,7 +776,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   // A workgroup has at most two parts of sequences that it shares: its first
   // and its last.
   const int64_t part_size = static_cast<int64_t>(min(kHeadTile, a.group)) * PR;
-  float* mine = a.part + (2 * blockIdx.x + (first ? 0 : 1)) * part_size;
+  float* mine = a.part + (2 * block + (first ? 0 : 1)) * part_size;
   for (int i = tid; i < heads * DP; i += kThreads) {
     const int r = i / DP, d = i % DP;
     float top = -INFINITY;
@@ -983,6 +1023,15 @@ DecodeArgs fill(const RowsView& out, const RowsView& q, int64_t heads, const xq_
   a.window = static_cast<int>(window);
   a.sinks = static_cast<int>(sinks);
   a.c = scale * kv.k_scale * kLog2e;
+  if (kv.dtype == kE2M1) {
+    a.ke_page = static_cast<uint32_t>(kv.k_exp_stride[1] / 4);
+    a.ke_tok = static_cast<uint32_t>(kv.k_exp_stride[3] / 4);
+    a.ve_page = static_cast<uint32_t>(kv.v_exp_stride[1] / 4);
+    a.ve_tok = static_cast<uint32_t>(kv.v_exp_stride[3] / 4);
+    a.flip = a.c < 0.f;
+    a.zero = a.c == 0.f;
+    a.c = a.zero ? 1.f : std::fabs(a.c);
+  }
   a.v_scale = kv.v_scale;
   return a;
 }

@@ -107,6 +107,13 @@ xq_status check_attention(int64_t heads, const xq_kv* kv, float scale, int64_t w
     if (last * static_cast<double>(xq::cache_bytes(2, kv->dtype)) / 2 >= 68719476736.0)
       return fail(XQ_E_SHAPE, "kv pages of one layer reach over 64 GiB");
   }
+  if (kv->dtype == XQ_E2M1)
+    for (const int64_t* st : {kv->k_exp_stride, kv->v_exp_stride}) {
+      // ... and its exponents in dwords.
+      const double last = static_cast<double>(kv->pages - 1) * static_cast<double>(st[1]) +
+                          static_cast<double>(kv->page - 1) * static_cast<double>(st[3]);
+      if (last >= 17179869184.0) return fail(XQ_E_SHAPE, "kv exponents of one layer reach over 16 GiB");
+    }
   if (window < 0 || window > kMaxLen)
     return fail(XQ_E_SHAPE, "window=%lld outside 0..2^30", (long long)window);
   if (sinks < 0 || sinks > kMaxLen)
