@@ -51,8 +51,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kTile = 32;                   // tokens of a wave's step
-constexpr int kStep = kTile * kWaves;       // tokens of a workgroup's step
+// Tokens of a wave's step, and of a workgroup's. (Of 4 bits twice as many: what a
+// step costs beside its products is shared by more, and as many bytes are under way.)
+constexpr int tile_of(int ct) { return ct == kE2M1 ? 64 : 32; }
+constexpr int step_of(int ct) { return tile_of(ct) * kWaves; }
 constexpr int kHeadTile = 16;               // heads of one workgroup
 constexpr int kCounterStride = 32;          // ints: a 128-byte line per arrival counter
 constexpr int kMaxGroups = 768;             // workgroups that share: 96 KiB of counters in every plan
@@ -117,7 +119,11 @@ __device__ __forceinline__ void lanes_meet() {
 }
 
 // Bits 0 .. n-1.
-__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0 : n >= 32 ? ~0u : (1u << n) - 1; }
+template <class M>
+__device__ __forceinline__ M below(int n) {
+  constexpr int kBits = 8 * sizeof(M);
+  return n <= 0 ? 0 : n >= kBits ? ~M{0} : (M{1} << n) - 1;
+}
 
 // V's loads are whole rows that nothing reads again: non-temporal ones take
 // 131072 tokens x 2 from 190 to 174 us. K's take part of a row's line each, and
@@ -168,11 +174,18 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   constexpr int VC = decode_v_loads(DP);
   constexpr int VB = F4 ? VE / 2 : VE * EB;        // its bytes
   constexpr int NE = DP > 128 ? 2 : 1;             // dwords of a row's exponents
+  constexpr int kTile = tile_of(CT), kStep = step_of(CT);
+  constexpr int TB = kTile / 16;                   // 16-token parts of a tile
+  constexpr int TV = kTile / 4;                    // tokens of a lane's V
+  using Mask = std::conditional_t<kTile == 64, uint64_t, uint32_t>;
+  constexpr Mask kAll = ~Mask{0};
   constexpr int OS = DP + 4;                       // floats of a joined row in LDS
   extern __shared__ float lds[];
-  __shared__ __attribute__((aligned(16))) uint32_t places[kWaves][2][kTile];
+  __shared__ __attribute__((aligned(16))) uint32_t places[kWaves][2][tile_of(CT)];
   // Of 4 bits: the powers of two of a tile's rows of k and of v.
-  __shared__ __attribute__((aligned(16))) float powers[F4 ? kWaves : 1][2][DP / 32][kTile];
+  __shared__ __attribute__((aligned(16))) float powers[F4 ? kWaves : 1][2][DP / 32][64];
+  // ... and q, which all waves have alike, in place of registers.
+  __shared__ u32x4 q_lds[F4 ? QS * NQ : 1][kWave];
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int l16 = lane % 16, lg = lane / 16;
@@ -306,17 +319,10 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     const int page = table[u < end ? at : 0];
     return u < end ? page : -1;
   };
-  uint32_t live;  // bit t: token t of the tile is there
+  Mask live;  // bit t: token t of the tile is there
   uint32_t k_at = 0, v_at = 0;
-  // Of 4 bits: lanes 0..31 read the exponents of k for the tile's tokens, the
-  // others those of v.
-  const uint8_t* eb = nullptr;
-  uint32_t e_at = 0, e_page = 0, e_tok = 0;
-  if constexpr (F4) {
-    eb = lane < kTile ? a.exps.k + kvh * a.exps.k_head : a.exps.v + kvh * a.exps.v_head;
-    e_page = lane < kTile ? a.ke_page : a.ve_page;
-    e_tok = lane < kTile ? a.ke_tok : a.ve_tok;
-  }
+  // Of 4 bits: where the exponents of the lane's token are, in dwords.
+  uint32_t ke_at = 0, ve_at = 0;
   auto place = [&](int u0, int page) {
     const int u = u0 + lane % kTile;
     const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.kv.pages);
@@ -327,23 +333,25 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     // and its v is cleared.
     k_at = ok ? page * a.k_page16 + slot * a.k_tok16 : k_at;
     v_at = ok ? page * a.v_page16 + slot * a.v_tok16 : v_at;
-    if constexpr (F4) e_at = ok ? page * e_page + slot * e_tok : e_at;
+    if constexpr (F4) {
+      ke_at = ok ? page * a.ke_page + slot * a.ke_tok : ke_at;
+      ve_at = ok ? page * a.ve_page + slot * a.ve_tok : ve_at;
+    }
     lanes_meet();
     places[wave][0][lane % kTile] = k_at;
     places[wave][1][lane % kTile] = v_at;
     lanes_meet();
-    live = static_cast<uint32_t>(__ballot(ok));
-    if constexpr (F4) live = __builtin_amdgcn_readfirstlane(live);
+    live = static_cast<Mask>(__ballot(ok));
   };
-  u32x4 kr[2][KN];
-  std::conditional_t<F4, uint32_t, u32x4> vr[VC][8];
-  uint32_t er[NE];  // of 4 bits: this lane's row of exponents
+  u32x4 kr[TB][KN];
+  std::conditional_t<F4, uint32_t, u32x4> vr[VC][TV];
+  uint32_t ker[NE], ver[NE];  // of 4 bits: the exponents of the lane's token
   auto load_k = [&]() {
-    uint32_t at[2];
+    uint32_t at[TB];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) at[t] = places[wave][0][t * 16 + l16];
+    for (int t = 0; t < TB; ++t) at[t] = places[wave][0][t * 16 + l16];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < TB; ++t) {
       const uint8_t* p = kb + static_cast<uint64_t>(at[t]) * 16;
 #pragma unroll
       for (int s = 0; s < KN; ++s) {
@@ -361,17 +369,22 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       }
     }
     if constexpr (F4) {
+      const uint8_t* ke = a.exps.k + kvh * a.exps.k_head + static_cast<uint64_t>(ke_at) * 4;
+      const uint8_t* ve = a.exps.v + kvh * a.exps.v_head + static_cast<uint64_t>(ve_at) * 4;
 #pragma unroll
-      for (int i = 0; i < NE; ++i) er[i] = reinterpret_cast<const uint32_t*>(eb + static_cast<uint64_t>(e_at) * 4)[i];
+      for (int i = 0; i < NE; ++i) {
+        ker[i] = reinterpret_cast<const uint32_t*>(ke)[i];
+        ver[i] = reinterpret_cast<const uint32_t*>(ve)[i];
+      }
     }
   };
   auto load_v = [&]() {
-    u32x4 at[2];
+    u32x4 at[TB];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < TB; ++t)
       at[t] = *reinterpret_cast<const u32x4*>(&places[wave][1][t * 16 + lg * 4]);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
+    for (int t = 0; t < TV; ++t) {
       const uint8_t* p = vb + static_cast<uint64_t>(at[t / 4][t % 4]) * 16;
 #pragma unroll
       for (int c = 0; c < VC; ++c) {  // (what stands for dims past the end nothing uses)
@@ -381,18 +394,20 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       }
     }
   };
-  // Of 4 bits: the powers of the lane's eight tokens of V, for its dims.
-  float vp[VC][8];
-  auto widen_v = [&](int c, u32x4(&w)[8]) {
+  // Of 4 bits: the powers of the lane's tokens of V, for its dims.
+  float vp[VC][TV];
+  // Eight tokens of the tile's part h of 32.
+  auto widen_v = [&](int c, int h, u32x4(&w)[8]) {
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
+    for (int i = 0; i < 8; ++i) {
+      const int t = h * 8 + i;
       if constexpr (F4) {
-        w[t] = widen8<MT>(vr[c][t], vp[c][t]);
+        w[i] = widen8<MT>(vr[c][t], vp[c][t]);
       } else if constexpr (CT == kE4M3) {
         const u32x2 x = widen4<MT>(vr[c][t].x), y = widen4<MT>(vr[c][t].y);
-        w[t] = u32x4{x.x, x.y, y.x, y.y};
+        w[i] = u32x4{x.x, x.y, y.x, y.y};
       } else {
-        w[t] = vr[c][t];
+        w[i] = vr[c][t];
       }
     }
   };
@@ -410,8 +425,8 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
   // q as the B operand: head l16, dims of step s. An f16 operand is scaled by
   // a power of two that brings the head's largest |q| to 2^14..2^15, so that
   // no piece of an f32 or bf16 q leaves f16's range.
-  u32x4 qf[QS][NQ];
   float qs = a.c;
+  u32x4 qf[QS][NQ];
   {
     float x[QS][8];
     float top = 0.f;
@@ -481,22 +496,31 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       }
   }
 
+  if constexpr (F4) {
+#pragma unroll
+    for (int s = 0; s < QS; ++s)
+#pragma unroll
+      for (int p = 0; p < NQ; ++p) q_lds[s * NQ + p][lane] = qf[s][p];
+    lanes_meet();
+  }
   // The loads of the next tile are not conditional (past the last, its tokens
   // are not there and read what was read before): the compiler then knows how
   // many are under way and waits for no more than it needs.
   while (u0 < end) {  // wave-uniform
-    const uint32_t here = live;
-    float kp[2][KN];  // of 4 bits: the powers of the lane's K
+    const Mask here = live;
+    float kp[TB][KN];  // of 4 bits: the powers of the lane's K
     if constexpr (F4) {
       // The rows' powers go through LDS to the lanes that hold their codes.
       lanes_meet();
 #pragma unroll
-      for (int b = 0; b < DP / 32; ++b)
-        powers[wave][lane / kTile][b][lane % kTile] = block_power((er[b / 4] >> (b % 4 * 8)) & 0xff);
+      for (int b = 0; b < DP / 32; ++b) {
+        powers[wave][0][b][lane] = block_power((ker[b / 4] >> (b % 4 * 8)) & 0xff);
+        powers[wave][1][b][lane] = block_power((ver[b / 4] >> (b % 4 * 8)) & 0xff);
+      }
       lanes_meet();
       constexpr int kBlocks = KL == 4 ? 1 : 2;  // K loads of a block
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < TB; ++t)
 #pragma unroll
         for (int s = 0; s < KN; ++s)
           kp[t][s] = powers[wave][0][min((s * 4 + lg) / kBlocks, DP / 32 - 1)][t * 16 + l16];
@@ -504,20 +528,22 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       for (int c = 0; c < VC; ++c) {
         const int b = min((c * 16 + l16) * VE / 32, DP / 32 - 1);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < TB; ++t) {
           const f32x4 e = *reinterpret_cast<const f32x4*>(&powers[wave][1][b][t * 16 + lg * 4]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) vp[c][t * 4 + i] = e[i];
         }
       }
     }
-    f32x4 st[2] = {zero4, zero4};
+    f32x4 st[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) st[t] = zero4;
 #pragma unroll
     for (int s = 0; s < QS; ++s)
 #pragma unroll
       for (int p = 0; p < NQ; ++p)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < TB; ++t) {
           u32x4 kf;
           if constexpr (F4) {
             kf = widen8<MT>(kr[t][s / KL][s % KL], kp[t][s / KL]);
@@ -533,14 +559,15 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
             const int d0 = (s / KL * 4 + lg) * 8 * KL + s % KL * 8;
             if (d0 >= a.dim) kf = u32x4{0, 0, 0, 0};
           }
-          st[t] = mfma16<MT>(kf, qf[s][p], st[t]);
+          if constexpr (F4) st[t] = mfma16<MT>(kf, q_lds[s * NQ + p][lane], st[t]);
+          else st[t] = mfma16<MT>(kf, qf[s][p], st[t]);
         }
     place(u0 + kStep, page);
     page = page_of(u0 + 2 * kStep);
     load_k();
 
     // Which of the tile's tokens this lane's row sees.
-    uint32_t sees = here;
+    Mask sees = here;
     bool same = true;  // for all rows
     if constexpr (CHUNK) {
       const int u = u0;
@@ -549,26 +576,27 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       if (!same) {
         // Bit k is token u + k where that is a sink, else token j + k.
         const int j = lo + u - ns;
-        const uint32_t sink = below(ns - u) & below(pos + 1 - u);
-        const uint32_t rest = ~below(ns - u) & below(pos + 1 - j) &
-                              (a.window ? ~below(pos - a.window + 1 - j) | below(sinks - j) : ~0u);
+        const Mask sink = below<Mask>(ns - u) & below<Mask>(pos + 1 - u);
+        const Mask rest = ~below<Mask>(ns - u) & below<Mask>(pos + 1 - j) &
+                          (a.window ? ~below<Mask>(pos - a.window + 1 - j) | below<Mask>(sinks - j) : kAll);
         sees = sink | rest;
         sees &= here;
       }
     }
-    float s[8];
+    float s[TV];
     float top = -INFINITY;
     if constexpr (F4) {
       // The scale is above 0: the largest score is the largest product's, and
       // scaling and subtraction are one instruction. Most tiles hide nothing.
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = st[i / 4][i % 4];
-      if (CHUNK ? __ballot(sees != ~0u) != 0 : here != ~0u) {
+      for (int i = 0; i < TV; ++i) s[i] = st[i / 4][i % 4];
+      if (CHUNK ? __ballot(sees != kAll) != 0 : here != kAll) {
+        const Mask mine = sees >> (lg * 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = (sees >> ((i / 4) * 16 + lg * 4 + i % 4)) & 1 ? s[i] : -INFINITY;
+        for (int i = 0; i < TV; ++i) s[i] = (mine >> ((i / 4) * 16 + i % 4)) & 1 ? s[i] : -INFINITY;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, s[i]);
+      for (int i = 0; i < TV; ++i) top = fmaxf(top, s[i]);
       top = fmaxf(m, swapped_max(top) * qs);
     } else {
 #pragma unroll
@@ -584,7 +612,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     m = top;
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < TV; ++i) {
       s[i] = F4 ? exp2_fast(fmaf(s[i], qs, -base)) : exp2_fast(s[i] - base);
       sum += s[i];
     }
@@ -595,9 +623,9 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
         for (int j = 0; j < VE; ++j) o[c][j] *= alpha;
     }
-    u32x4 pf[NP];
+    u32x4 pf[TV / 8][NP];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
+    for (int i = 0; i < TV; i += 2) {
       // f16 pieces of weights up to 2^14, so that small ones keep their bits
       // (the join divides the factor out).
       float u = s[i], w = s[i + 1];
@@ -608,16 +636,16 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         const uint32_t h = pack2<MT>(u, w);
-        pf[p][i / 2] = h;
+        pf[i / 8][p][i % 8 / 2] = h;
         const f32x2 back = unpack2<MT>(h);
         u -= back.x;
         w -= back.y;
       }
     }
-    if (here != 0xffffffffu) {
+    if (here != kAll) {
       // What lies in a place without a token may be anything, NaN too.
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
+      for (int t = 0; t < TV; ++t)
         if (!((here >> ((t / 4) * 16 + lg * 4 + t % 4)) & 1))
 #pragma unroll
           for (int c = 0; c < VC; ++c) {
@@ -636,7 +664,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
         for (int c = 0; c < VC; ++c)
 #pragma unroll
-          for (int t = 0; t < 8; ++t) any |= vp[c][t] == INFINITY;
+          for (int t = 0; t < TV; ++t) any |= vp[c][t] == INFINITY;
         odd = __ballot(any) != 0;
       }
     } else if (CT != kE4M3 || !same) {
@@ -644,7 +672,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
       for (int c = 0; c < VC; ++c)
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < TV; ++t)
 #pragma unroll
           for (int i = 0; i < VE * EB / 4; ++i) carry |= (vr[c][t][i] & ~kSigns) + kOne;
       odd = __ballot(carry & kSigns) != 0;
@@ -655,7 +683,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
       for (int c = 0; c < VC; ++c)
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
+        for (int t = 0; t < TV; ++t) {
           if constexpr (F4) {
             if (vp[c][t] == INFINITY) vp[c][t] = 0.f, vr[c][t] = 0;
           } else {
@@ -709,16 +737,19 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     if (!odd) {
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
-        u32x4 vw[8];
-        widen_v(c, vw);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const u32x4 vf = turned(vw, j, 0);
+        for (int h = 0; h < TV / 8; ++h) {
+          u32x4 vw[8];
+          widen_v(c, h, vw);
 #pragma unroll
-          for (int p = 0; p < NP; ++p) o[c][j] = mfma16<MT>(vf, pf[p], o[c][j]);
+          for (int j = 0; j < VE; ++j) {
+            const u32x4 vf = turned(vw, j, 0);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) o[c][j] = mfma16<MT>(vf, pf[h][p], o[c][j]);
+          }
         }
       }
-    } else {
+    } else if constexpr (!F4) {
       // An infinity times p's first piece is the infinity it should be; times
       // a further piece, which may be 0 or below, it is not. (The zero that the
       // compiler does not know keeps this path's turning of V its own: shared
@@ -728,14 +759,14 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
         u32x4 vw[8];
-        widen_v(c, vw);
+        widen_v(c, 0, vw);
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
           const u32x4 vf = turned(vw, j, flip);
           f32x4 x = zero4;
 #pragma unroll
-          for (int p = 1; p < NP; ++p) x = mfma16<MT>(vf, pf[p], x);
-          o[c][j] = mfma16<MT>(vf, pf[0], o[c][j]);
+          for (int p = 1; p < NP; ++p) x = mfma16<MT>(vf, pf[0][p], x);
+          o[c][j] = mfma16<MT>(vf, pf[0][0], o[c][j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             o[c][j][i] += fabsf(x[i]) < INFINITY ? x[i] : 0.f;
@@ -929,11 +960,11 @@ Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t
   Plan p;
   p.per_seq = units_of(heads, kv);
   const int64_t most = window && window + sinks < max_len ? window + sinks : max_len;
-  const int64_t steps = (most + kStep - 1) / kStep;
+  const int64_t steps = (most + step_of(kv.dtype) - 1) / step_of(kv.dtype);
   const int dp = decode_dim_pad(static_cast<int>(kv.dim));
-  const bool apart = dp == 128 && kv.k_stride[3] != kv.dim && kv.page > 1;
+  const bool apart = dp == 128 && kv.dtype != kE2M1 && kv.k_stride[3] != kv.dim && kv.page > 1;
   const int64_t room = 256 * (apart ? 1 : groups_per_cu(kv.dtype, dp));
-  p.shared = steps > 3 && seqs * p.per_seq < 3 * room && p.per_seq <= room && seqs * steps < (1 << 30);
+  p.shared = steps > (kv.dtype == kE2M1 ? 1 : 3) && seqs * p.per_seq < 3 * room && p.per_seq <= room && seqs * steps < (1 << 30);
   p.ranges = p.shared ? std::min(room / p.per_seq, seqs * steps) : seqs;
   return p;
 }
