@@ -41,7 +41,7 @@ __device__ __forceinline__ float4 load_x4(const uint8_t* row, int type, int at) 
 
 // ---------------------------------------------------------------- router
 
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512;
 constexpr int kRouteWaves = kRouteThreads / kWave;
 constexpr int kRouteExperts = 4;  // of a workgroup
 
@@ -93,7 +93,7 @@ __device__ __forceinline__ Row8 load_x8(const uint8_t* row, int type, int at) {
 // lowest index among equals. PER: experts of a lane there.
 template <int NT, int PER>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
-  __shared__ float sums[kRouteWaves][kRouteExperts * NT];
+  __shared__ float sums[kRouteWaves * 4][kRouteExperts * NT];
   __shared__ int last;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int tile = blockIdx.x / a.expert_tiles, e0 = blockIdx.x % a.expert_tiles * kRouteExperts;
@@ -118,14 +118,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   for (int e = 0; e < kRouteExperts; ++e)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const float v = wave_sum(sum[e][t]);
-      if (lane == 0) sums[wave][e * NT + t] = v;
+      const float v = row16_sum(sum[e][t]);
+      if (lane % 16 == 0) sums[threadIdx.x / 16][e * NT + t] = v;
     }
   __syncthreads();
   if (threadIdx.x < kRouteExperts * NT) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w) v += sums[w][threadIdx.x];
+    for (int w = 0; w < kRouteWaves * 4; ++w) v += sums[w][threadIdx.x];
     const int e = e0 + threadIdx.x / NT, t = threadIdx.x % NT;
     if (e < a.experts && t < tokens)
       __hip_atomic_store(a.logits + static_cast<int64_t>(t0 + t) * a.experts + e, v, __ATOMIC_RELAXED,
@@ -140,7 +140,6 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   if (!last) return;  // workgroup-uniform
   if (threadIdx.x == 0)
     __hip_atomic_store(a.count + tile * kCounterStride, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
 
   for (int t = wave; t < tokens; t += kRouteWaves) {
     const float* logits = a.logits + static_cast<int64_t>(t0 + t) * a.experts;
@@ -150,7 +149,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int e = j * kWave + lane;
-      score[j] = e < a.experts ? logits[e] : -INFINITY;
+      score[j] = e < a.experts ? __hip_atomic_load(logits + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : -INFINITY;
       top = fmaxf(top, score[j]);
     }
     float all = 1.f;
@@ -180,7 +179,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         if (key[j] > best) best = key[j], at = j, s = score[j];
       const int high = wave_max_int(best);
       // Of the lanes that have it the one with the lowest index.
-      const int id = -wave_max_int(best == high ? -(at * kWave + lane) : kAbsent + 1);
+      const uint64_t have = __ballot(best == high);
+      int id = __builtin_ctzll(have);
+      if constexpr (PER > 1) {
+        if (have & (have - 1)) id = -wave_max_int(best == high ? -(at * kWave + lane) : kAbsent + 1);
+        else id += __builtin_amdgcn_readlane(at, id) * kWave;
+      }
       const float v = readlane(s, id % kWave);
 #pragma unroll
       for (int j = 0; j < PER; ++j)
@@ -247,7 +251,7 @@ constexpr int up_rows(int nt, int lpr) { return up_steps(nt) * (kWave / lpr) / 2
 // (nb <= LPR / 4 where it is below 64). A workgroup has W waves, each `groups`
 // times R rows of h, of the expert of pair blockIdx.y.
 template <int NT, int LPR, int W>
-__global__ __launch_bounds__(W * kWave) void moe_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(W * kWave, 3) void moe_up_kernel(MoeArgs a) {
   constexpr int SEG = kWave / LPR;            // rows of weights of a wave at a time
   constexpr int STEPS = up_steps(NT);
   constexpr int R = up_rows(NT, LPR);
@@ -256,6 +260,14 @@ __global__ __launch_bounds__(W * kWave) void moe_up_kernel(MoeArgs a) {
   __shared__ uint16_t members[NT > 1 ? kMaxPairs : 1];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int pair = blockIdx.y;
+  // One token's x does not wait for the choice of experts. (Two blocks a wave;
+  // 16 blocks, 4096 columns, have more.)
+  constexpr int XE = NT == 1 ? 2 : 1;
+  float4 xe[XE];
+  if constexpr (NT == 1) {
+#pragma unroll
+    for (int i = 0; i < XE; ++i) xe[i] = load_x4(a.x, a.x_type, min(wave + i * W, a.nb - 1) * 256 + lane * 4);
+  }
   const int e = a.ids[pair];
   if (e < 0 || e >= a.experts) return;
   int count = 1;
@@ -288,7 +300,12 @@ __global__ __launch_bounds__(W * kWave) void moe_up_kernel(MoeArgs a) {
     uint4 h0[STEPS], h1[STEPS];
     load(0, 0, n0, h0);
     if (NT > 1) __syncthreads();  // the members are listed; the pass before is done with the activations
-    for (int i = wave; i < here * a.nb; i += W) {
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int i = 0; i < XE; ++i)
+        if (wave + i * W < a.nb) q8k_block_wave<true>(xe[i], act + (wave + i * W) * kQ8KBytes, lane);
+    }
+    for (int i = wave + (NT == 1 ? XE * W : 0); i < here * a.nb; i += W) {
       const int t = NT > 1 ? div_by(i, a.nb_div) : 0, b = i - t * a.nb;
       const uint8_t* row = a.x + div_by(member(m + t), a.used_div) * a.x_row;
       q8k_block_wave<true>(load_x4(row, a.x_type, b * 256 + lane * 4), act + i * kQ8KBytes, lane);
@@ -364,57 +381,107 @@ __global__ __launch_bounds__(W * kWave) void moe_up_kernel(MoeArgs a) {
 }
 
 // Down for a token by itself: a wave's row of y is one sum over the blocks of
-// all its slots' rows, four lanes a block, 16 blocks at a time. The workgroup
-// quantizes the token's h, used * nb blocks, while its first weights load.
-template <int W>
+// all its slots' rows, four lanes a block, 16 blocks at a time; `groups` rows one
+// after the other. The workgroup quantizes the token's h, used * nb blocks, while
+// its first weights load.
+// PF: steps of 16 blocks under way, all of a row's up to four.
+template <int W, int PF>
 __global__ __launch_bounds__(W * kWave) void moe_down_kernel(MoeArgs a) {
-  constexpr int PF = 4;
+  constexpr int QB = 3;     // blocks of a wave quantized side by side
   extern __shared__ __attribute__((aligned(16))) uint8_t act[];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int token = blockIdx.y, row = blockIdx.x * W + wave;
+  const int token = blockIdx.y;
   const LaneGeom L = lane_geom(lane);
   const int blocks = a.used * a.nb, steps = (blocks + kUnitBlocks - 1) / kUnitBlocks;
+  const int batches = (steps + PF - 1) / PF;
   const int64_t row_bytes = static_cast<int64_t>(a.nb) * kQ4KBytes;
-  Nib nib[PF];
-  uint4 hdr[PF];
-  float weight[PF];  // of the slot
-  bool there[PF];
-  auto load = [&](int s0) {
+  struct Batch {
+    Nib nib[PF];
+    uint4 hdr[PF];
+  };
+  const int first = blockIdx.x * a.groups * W + wave;
+  // A lane's blocks of a batch: which slot's, of which expert, its weight.
+  int place[PF], expert[PF];
+  float weight[PF];
+  auto look_up = [&](int bt) {
 #pragma unroll
     for (int p = 0; p < PF; ++p) {
-      const int i = (s0 + p) * kUnitBlocks + L.bsub, k = div_by(min(i, blocks - 1), a.nb_div);
+      const int i = (bt * PF + p) * kUnitBlocks + L.bsub, k = div_by(min(i, blocks - 1), a.nb_div);
       const int e = a.ids[token * a.used + k];
-      there[p] = i < blocks && row < a.rows && e >= 0 && e < a.experts;
       weight[p] = a.weights[token * a.used + k];
-      nib[p] = zero_group();
-      hdr[p] = make_uint4(0, 0, 0, 0);
-      if (there[p]) {
-        const uint8_t* blk = a.w[0] + (static_cast<int64_t>(e) * a.rows + row) * row_bytes + (i - k * a.nb) * kQ4KBytes;
-        nib[p] = load_group(blk, L);
-        hdr[p] = *reinterpret_cast<const uint4*>(blk);
+      expert[p] = i < blocks && e >= 0 && e < a.experts ? e : -1;
+      place[p] = min(i, blocks - 1) - k * a.nb;
+    }
+  };
+  auto load = [&](int row, Batch& b) {
+#pragma unroll
+    for (int p = 0; p < PF; ++p) {
+      b.nib[p] = zero_group();
+      b.hdr[p] = make_uint4(0, 0, 0, 0);
+      if (expert[p] >= 0 && row < a.rows) {
+        const uint8_t* blk = a.w[0] + (static_cast<int64_t>(expert[p]) * a.rows + row) * row_bytes + place[p] * kQ4KBytes;
+        b.nib[p] = load_group(blk, L);
+        b.hdr[p] = *reinterpret_cast<const uint4*>(blk);
       }
     }
   };
-  load(0);
+  look_up(0);
+  Batch b0, b1;
+  load(first, b0);
   const float* h = reinterpret_cast<const float*>(a.x) + static_cast<int64_t>(token) * blocks * 256;
-  for (int i = wave; i < blocks; i += W) {
-    const int e = a.ids[token * a.used + div_by(i, a.nb_div)];
-    if (e < 0 || e >= a.experts) continue;  // wave-uniform; its h was not written
-    q8k_block_wave<true>(*reinterpret_cast<const float4*>(h + i * 256 + lane * 4), act + i * kQ8KBytes, lane);
+  for (int i0 = wave; i0 < blocks; i0 += QB * W) {
+    float4 v[QB];
+    bool ok[QB];  // (the h of a slot that is left out was not written)
+#pragma unroll
+    for (int q = 0; q < QB; ++q) {
+      const int i = min(i0 + q * W, blocks - 1), e = a.ids[token * a.used + div_by(i, a.nb_div)];
+      ok[q] = i0 + q * W < blocks && e >= 0 && e < a.experts;
+      v[q] = ok[q] ? *reinterpret_cast<const float4*>(h + i * 256 + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int q = 0; q < QB; ++q)
+      if (ok[q]) q8k_block_wave<true>(v[q], act + (i0 + q * W) * kQ8KBytes, lane);
   }
   __syncthreads();
   float acc = 0.f;
-  for (int s0 = 0; s0 < steps; s0 += PF) {
-    if (s0) load(s0);
+  auto add = [&](int bt, const Batch& b) {
 #pragma unroll
     for (int p = 0; p < PF; ++p) {
-      const int i = min((s0 + p) * kUnitBlocks + L.bsub, blocks - 1);
-      const float v = unit_partial(nib[p], hdr[p], act, i, L);
-      if (there[p]) acc = fmaf(weight[p], v, acc);
+      const int i = min((bt * PF + p) * kUnitBlocks + L.bsub, blocks - 1);
+      const float v = unit_partial(b.nib[p], b.hdr[p], act, i, L);
+      if (expert[p] >= 0) acc = fmaf(weight[p], v, acc);
+    }
+  };
+  auto store = [&](int row) {
+    const float sum = wave_sum(acc);
+    acc = 0.f;
+    if (lane == 0 && row < a.rows) store_from_f32(a.y + token * a.y_row, a.type, row, sum);
+  };
+  if (PF < 4 || batches == 1) {
+    // The next row's weights load while one is worked on.
+    for (int g = 0; g < a.groups; g += 2) {
+      const int row = first + g * W;
+      if (g + 1 < a.groups) load(row + W, b1);
+      add(0, b0);
+      store(row);
+      if (g + 1 >= a.groups) break;
+      if (g + 2 < a.groups) load(row + 2 * W, b0);
+      add(0, b1);
+      store(row + W);
+    }
+  } else {
+    for (int g = 0; g < a.groups; ++g) {
+      const int row = first + g * W;
+      for (int bt = 0; bt < batches; ++bt) {
+        if (g > 0 || bt > 0) {
+          look_up(bt);
+          load(row, b0);
+        }
+        add(bt, b0);
+      }
+      store(row);
     }
   }
-  const float sum = wave_sum(acc);
-  if (lane == 0 && row < a.rows) store_from_f32(a.y + token * a.y_row, a.type, row, sum);
 }
 
 // ---- Many pairs an expert: matrix instructions.
@@ -493,35 +560,39 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void moe_tile_kernel(MoeArgs
     Weights w0, w1;
     load(0, w0);
     __syncthreads();  // the members are listed; the pass before is done with the activations
-    // Word i of a chunk: of pair i / kWords / kChunk. (Rows of pairs past the last
-    // stay as they are; what they give nothing reads.)
+    // A thread's words of a chunk: word i is pair i / kChunk / kWords's. Nothing
+    // here is conditional, so that the compiler knows how many loads are under
+    // way: past the last word it is that one again, past the last chunk too. (Rows of
+    // pairs past the last stay as they are; what they give nothing reads. The
+    // block after a row of an odd number is the workspace's, and not used.)
     const int words = here * kChunk * kWords;
-    u32x4 st[kPer];
-    float ss = 0.f;
     auto row_of = [&](int t) {
       const int p = members[m0 + t];
-      return a.by_pair ? p : static_cast<int>(div_by(p, a.used_div));
+      return static_cast<uint32_t>((a.by_pair ? p : static_cast<int>(div_by(p, a.used_div))) * a.nb);
     };
+    uint32_t from[kPer], to[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = min(tid + j * kThreads, words - 1);
+      const int t = i / (kChunk * kWords), r = i % (kChunk * kWords);
+      from[j] = row_of(t) * kPackBytes + r * 16;
+      to[j] = (r / kWords * kTilePairs + t) * kPackRow + r % kWords * 16;
+    }
+    const int mine = min(tid, here * kChunk - 1);
+    const uint32_t scale_from = row_of(mine / kChunk) + mine % kChunk;
+    u32x4 st[kPer];
+    float ss;
     auto fetch = [&](int c) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = tid + j * kThreads;
-        if (i >= words) break;
-        const int t = i / (kChunk * kWords), r = i % (kChunk * kWords), b = min(c * kChunk + r / kWords, a.nb - 1);
-        st[j] = reinterpret_cast<const u32x4*>(a.x + (static_cast<int64_t>(row_of(t)) * a.nb + b) * kPackBytes)[r % kWords];
-      }
-      if (tid < here * kChunk)
-        ss = a.xs[static_cast<int64_t>(row_of(tid / kChunk)) * a.nb + min(c * kChunk + tid % kChunk, a.nb - 1)];
+      for (int j = 0; j < kPer; ++j)
+        st[j] = *reinterpret_cast<const u32x4*>(a.x + (from[j] + static_cast<uint32_t>(c * kChunk * kPackBytes)));
+      ss = a.xs[scale_from + c * kChunk];
     };
     auto put = [&](int c) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = tid + j * kThreads;
-        if (i >= words) break;
-        const int t = i / (kChunk * kWords), r = i % (kChunk * kWords);
-        *reinterpret_cast<u32x4*>(&act[c % 2][r / kWords][t * kPackRow + r % kWords * 16]) = st[j];
-      }
-      if (tid < here * kChunk) scale[c % 2][tid % kChunk][tid / kChunk] = ss;
+      for (int j = 0; j < kPer; ++j)
+        *reinterpret_cast<u32x4*>(act[c % 2][0] + to[j]) = st[j];
+      scale[c % 2][mine % kChunk][mine / kChunk] = ss;
     };
     fetch(0);
     put(0);
@@ -576,17 +647,17 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void moe_tile_kernel(MoeArgs
       }
     };
     auto step = [&](int c, Weights& now, Weights& next) {
-      const bool more = c + 1 < chunks;
-      if (more) {
-        fetch(c + 1);
-        load(c + 1, next);
-      }
+      const int after = min(c + 1, chunks - 1);
+      fetch(after);
+      load(after, next);
       add(c, now);
-      if (more) put(c + 1);
+      put(c + 1);
       __syncthreads();
-      return more;
     };
-    for (int c = 0; step(c, w0, w1) && step(c + 1, w1, w0); c += 2) {
+    // (An odd number's last step adds nothing.)
+    for (int c = 0; c < chunks; c += 2) {
+      step(c, w0, w1);
+      step(c + 1, w1, w0);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -622,9 +693,10 @@ hipError_t launch_up(MoeArgs a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   const int64_t pairs = static_cast<int64_t>(a.tokens) * a.used;
-  // So many groups a wave that about four workgroups a CU remain.
+  // So many groups a wave that all workgroups are on the card at once.
+  constexpr int64_t kRoom = 256 * 3;
   const int64_t tiles = (a.rows + W * R - 1) / (W * R);
-  a.groups = static_cast<int>(std::clamp<int64_t>(tiles * pairs / 1024, 1, 16));
+  a.groups = static_cast<int>((tiles * pairs + kRoom - 1) / kRoom);
   const int64_t blocks = (tiles + a.groups - 1) / a.groups;
   kernel<<<dim3(static_cast<uint32_t>(blocks), static_cast<uint32_t>(pairs)), dim3(W * kWave), lds, stream>>>(a);
   return hipGetLastError();
@@ -654,6 +726,23 @@ hipError_t launch_pack(uint8_t* packed, float* scales, const uint8_t* x, int64_t
 }
 
 constexpr int kDownWaves = 8;
+template <int PF>
+hipError_t launch_down(MoeArgs a, hipStream_t stream) {
+  const size_t lds = static_cast<size_t>(a.used) * a.nb * kQ8KBytes;
+  auto kernel = moe_down_kernel<kDownWaves, PF>;
+  if (lds > 48 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+    if (e != hipSuccess) return e;
+  }
+  // So many rows a wave that all workgroups are on the card at once, one a CU.
+  const int per_token = std::max(1, 256 / a.tokens);
+  a.groups = (a.rows + per_token * kDownWaves - 1) / (per_token * kDownWaves);
+  const int blocks = (a.rows + a.groups * kDownWaves - 1) / (a.groups * kDownWaves);
+  kernel<<<dim3(static_cast<uint32_t>(blocks), static_cast<uint32_t>(a.tokens)), dim3(kDownWaves * kWave), lds, stream>>>(a);
+  return hipGetLastError();
+}
+
 // Mat-vecs, and down token by token, where tokens hardly share experts (as many
 // experts as pairs and more) and a token's h fits a workgroup's LDS.
 bool by_rows(int64_t tokens, int64_t used, int64_t experts, int64_t ffn) {
@@ -762,16 +851,11 @@ hipError_t launch_moe_q4k(void* y, int64_t y_row, const void* x, int64_t x_row, 
   hipError_t e;
   if (by_rows(tokens, used, experts, ffn)) {
     if ((e = tokens == 1 ? launch_lanes<1>(a, stream) : launch_lanes<2>(a, stream)) != hipSuccess) return e;
-    const size_t lds = static_cast<size_t>(used) * d.nb * kQ8KBytes;
-    if (lds > 48 * 1024) {
-      e = hipFuncSetAttribute(reinterpret_cast<const void*>(moe_down_kernel<kDownWaves>),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
-      if (e != hipSuccess) return e;
-    }
-    moe_down_kernel<kDownWaves><<<dim3(static_cast<uint32_t>((hidden + kDownWaves - 1) / kDownWaves),
-                                       static_cast<uint32_t>(tokens)),
-                                  dim3(kDownWaves * kWave), lds, stream>>>(d);
-    return hipGetLastError();
+    const int64_t steps = (used * d.nb + kUnitBlocks - 1) / kUnitBlocks;
+    if (steps == 1) return launch_down<1>(d, stream);
+    if (steps == 2) return launch_down<2>(d, stream);
+    if (steps == 3) return launch_down<3>(d, stream);
+    return launch_down<4>(d, stream);
   }
   a.xs = reinterpret_cast<const float*>(w + l.xs);
   if ((e = launch_pack(w + l.xp, reinterpret_cast<float*>(w + l.xs), a.x, a.x_row, io, tokens, a.nb, stream)) != hipSuccess)

@@ -27,9 +27,11 @@ struct Q8KLane {
   float d;
 };
 
-// PRODUCT: the scale is amax times 1/127 as f32 rounds it, where a workgroup
-// quantizes what it needs for itself (a division less; in 1 of 25 blocks the
-// scale's last bit is another).
+// PRODUCT: for workgroups that quantize what they need for themselves. The scale
+// is amax times 1/127 as f32 rounds it (in 1 of 25 blocks its last bit is
+// another). The codes are the quotients' all the same: x times the reciprocal is
+// off by less than 127 * 2^-21, and only where that is nearer than 1e-4 to the
+// middle between two codes does the wave divide.
 template <bool PRODUCT = false>
 __device__ __forceinline__ Q8KLane q8k_block_lane(const float4 v) {
   const float a = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
@@ -37,7 +39,24 @@ __device__ __forceinline__ Q8KLane q8k_block_lane(const float4 v) {
   const float d = PRODUCT ? amax * (1.0f / 127.0f) : amax / 127.0f;
 
   int q0 = 0, q1 = 0, q2 = 0, q3 = 0;
-  if (d != 0.0f) {
+  if constexpr (PRODUCT) {
+    // (A scale below f32's normal numbers has no reciprocal to go by.)
+    const bool fast = d >= 1.17549435e-38f && d <= 1e37f;
+    const float inv = fast ? __builtin_amdgcn_rcpf(d) : 0.0f;
+    const float r0 = v.x * inv, r1 = v.y * inv, r2 = v.z * inv, r3 = v.w * inv;
+    const float c0 = rintf(r0), c1 = rintf(r1), c2 = rintf(r2), c3 = rintf(r3);
+    const float far = fmaxf(fmaxf(fabsf(r0 - c0), fabsf(r1 - c1)), fmaxf(fabsf(r2 - c2), fabsf(r3 - c3)));
+    q0 = static_cast<int>(c0);
+    q1 = static_cast<int>(c1);
+    q2 = static_cast<int>(c2);
+    q3 = static_cast<int>(c3);
+    if (__ballot(!(far < 0.4999f)) || (!fast && d != 0.0f)) {  // wave-uniform
+      q0 = q8k_code(v.x, d);
+      q1 = q8k_code(v.y, d);
+      q2 = q8k_code(v.z, d);
+      q3 = q8k_code(v.w, d);
+    }
+  } else if (d != 0.0f) {
     q0 = q8k_code(v.x, d);
     q1 = q8k_code(v.y, d);
     q2 = q8k_code(v.z, d);
