@@ -501,6 +501,13 @@ constexpr int kPackRow = kPackBytes + 16;      // in LDS: 8 rows of 16-byte read
 constexpr int kTileWaves = 4;
 constexpr int kTilePairs = 16;
 constexpr int kChunk = 2;                      // blocks between two barriers
+// A wave's rows of weights of a chunk go through LDS: loaded as they lie, 18
+// lanes a row next to each other, read back a lane a row. (Loaded a lane a row,
+// four lanes of a quad touch four rows' cache lines in each of three loads: the
+// loads alone took 124 us for 528 MB.)
+constexpr int kRowBytes = kChunk * kQ4KBytes, kRowWords = kRowBytes / 16;
+constexpr int kRowPitch = kRowBytes + 16;      // 8 rows of 16-byte reads hit all banks
+constexpr int kRowLoads = (16 * kRowWords + kWave - 1) / kWave;
 
 // Rows of any type to packed blocks and their scales, a wave a block.
 __global__ __launch_bounds__(256) void moe_pack_kernel(uint8_t* packed, float* scales, const uint8_t* x, int64_t x_row,
@@ -526,6 +533,7 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void moe_tile_kernel(MoeArgs
   constexpr int kWords = kPackBytes / 16;                                     // 16-byte words of a packed block
   constexpr int kPer = (kTilePairs * kChunk * kWords + kThreads - 1) / kThreads;
   __shared__ __attribute__((aligned(16))) uint8_t act[2][kChunk][kTilePairs * kPackRow];
+  __shared__ __attribute__((aligned(16))) uint8_t rows[kTileWaves][MATS][16 * kRowPitch];
   __shared__ __attribute__((aligned(16))) float scale[2][kChunk][kTilePairs];
   __shared__ uint16_t members[kMaxPairs];
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, l16 = lane % 16, lg = lane / 16;
@@ -535,30 +543,44 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void moe_tile_kernel(MoeArgs
   const int count = pairs_of(a.ids, a.tokens * a.used, pair, e, members);
   if (count == 0) return;  // workgroup-uniform
   const LaneGeom L{0, lg, lg >= 2 ? ~0u : 0u, 16 * (lg & 1)};
-  const int row0 = (blockIdx.x * kTileWaves + wave) * 16, row = min(row0 + l16, a.rows - 1);
-  const int64_t row_at = (static_cast<int64_t>(e) * a.rows + row) * a.nb * kQ4KBytes;
+  const int row0 = (blockIdx.x * kTileWaves + wave) * 16;
+  const int row_bytes = a.nb * kQ4KBytes;
+  const int64_t rows_at = (static_cast<int64_t>(e) * a.rows + min(row0, a.rows - 1)) * row_bytes;
   const int chunks = (a.nb + kChunk - 1) / kChunk;
-
-  struct Weights {
-    Nib nib[MATS][kChunk];
-    uint4 hdr[MATS][kChunk];
-  };
-  auto load = [&](int c, Weights& w) {
+  // This lane's words of the wave's rows: word i is row i / kRowWords's. Rows past
+  // the matrix's last are that one again, words past a row's end its last.
+  uint32_t word_from[kRowLoads], word_in[kRowLoads], word_to[kRowLoads];
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) {
-      const int b = min(c * kChunk + k, a.nb - 1);
+  for (int j = 0; j < kRowLoads; ++j) {
+    const int i = min(lane + j * kWave, 16 * kRowWords - 1), r = i / kRowWords;
+    word_in[j] = i % kRowWords * 16;
+    word_from[j] = max(min(r, a.rows - 1 - row0), 0) * row_bytes;
+    word_to[j] = r * kRowPitch + word_in[j];
+  }
+  u32x4 raw[MATS][kRowLoads];
+  auto load = [&](int c) {
 #pragma unroll
-      for (int m = 0; m < MATS; ++m) {
-        const uint8_t* blk = a.w[m] + row_at + b * kQ4KBytes;
-        w.nib[m][k] = load_group(blk, L);
-        w.hdr[m][k] = *reinterpret_cast<const uint4*>(blk);
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+      for (int j = 0; j < kRowLoads; ++j) {
+        const uint32_t in = min(static_cast<uint32_t>(c * kRowBytes) + word_in[j], static_cast<uint32_t>(row_bytes - 16));
+        raw[m][j] = *reinterpret_cast<const u32x4*>(a.w[m] + rows_at + (word_from[j] + in));
       }
-    }
+  };
+  auto lay_out = [&]() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+      for (int j = 0; j < kRowLoads; ++j) *reinterpret_cast<u32x4*>(&rows[wave][m][word_to[j]]) = raw[m][j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
   };
   for (int m0 = 0; m0 < count; m0 += kTilePairs) {
     const int here = min(kTilePairs, count - m0);
-    Weights w0, w1;
-    load(0, w0);
+    load(0);
     __syncthreads();  // the members are listed; the pass before is done with the activations
     // A thread's words of a chunk: word i is pair i / kChunk / kWords's. Nothing
     // here is conditional, so that the compiler knows how many loads are under
@@ -601,7 +623,7 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void moe_tile_kernel(MoeArgs
     f32x4 total[MATS];
 #pragma unroll
     for (int m = 0; m < MATS; ++m) total[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto add = [&](int c, const Weights& w) {
+    auto add = [&](int c) {
 #pragma unroll
       for (int k = 0; k < kChunk; ++k) {
         if (c * kChunk + k >= a.nb) break;  // workgroup-uniform
@@ -612,7 +634,8 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void moe_tile_kernel(MoeArgs
 #pragma unroll
         for (int m = 0; m < MATS; ++m) {
           s[m] = low[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-          d[m] = chunk_decode(w.nib[m][k], w.hdr[m][k], L);
+          const uint8_t* blk = &rows[wave][m][l16 * kRowPitch + k * kQ4KBytes];
+          d[m] = chunk_decode(load_group(blk, L), *reinterpret_cast<const uint4*>(blk), L);
           const float s0 = static_cast<float>(d[m].sc0), s1 = static_cast<float>(d[m].sc1);
           sc[m] = u32x4{pack2<kF16>(s0, s0), pack2<kF16>(-1024.f * s0, -1024.f * s0),
                         pack2<kF16>(s1 * 0.0625f, s1 * 0.0625f), pack2<kF16>(-64.f * s1, -64.f * s1)};
@@ -646,18 +669,15 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void moe_tile_kernel(MoeArgs
             total[m][i] = fmaf(xs[i], fmaf(-d[m].dmin, low[m][i], d[m].d * s[m][i]), total[m][i]);
       }
     };
-    auto step = [&](int c, Weights& now, Weights& next) {
+    // The next chunk's loads are under way while one is worked on.
+    for (int c = 0; c < chunks; ++c) {
       const int after = min(c + 1, chunks - 1);
+      lay_out();
       fetch(after);
-      load(after, next);
-      add(c, now);
+      load(after);
+      add(c);
       put(c + 1);
       __syncthreads();
-    };
-    // (An odd number's last step adds nothing.)
-    for (int c = 0; c < chunks; c += 2) {
-      step(c, w0, w1);
-      step(c + 1, w1, w0);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
