@@ -127,7 +127,8 @@ __device__ __forceinline__ M below(int n) {
 
 // V's loads are whole rows that nothing reads again: non-temporal ones take
 // 131072 tokens x 2 from 190 to 174 us. K's take part of a row's line each, and
-// lose by it (32768 tokens x 8 stored token by token, 88 against 103 us).
+// lose by it (32768 tokens x 8 stored token by token, 88 against 103 us), and so
+// do V's of 4 bits, 64 bytes a row (32 sequences of up to 4099 35.5 against 37.5).
 template <int BYTES>
 __device__ __forceinline__ u32x4 load_words(const uint8_t* p) {
   if constexpr (BYTES == 16) {
@@ -135,10 +136,8 @@ __device__ __forceinline__ u32x4 load_words(const uint8_t* p) {
   } else if constexpr (BYTES == 8) {
     const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
     return u32x4{v.x, v.y, 0, 0};
-  } else if constexpr (BYTES == 4) {
-    return u32x4{__builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)), 0, 0, 0};
   } else {
-    return u32x4{__builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(p)), 0, 0, 0};
+    return u32x4{__builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)), 0, 0, 0};
   }
 }
 
@@ -389,7 +388,8 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
 #pragma unroll
       for (int c = 0; c < VC; ++c) {  // (what stands for dims past the end nothing uses)
         const int d0 = decode_v_dim<DP, FULL>(c, l16, a.dim);
-        if constexpr (F4) vr[c][t] = load_words<VB>(p + d0 / 2).x;
+        if constexpr (F4 && VB == 4) vr[c][t] = *reinterpret_cast<const uint32_t*>(p + d0 / 2);
+        else if constexpr (F4) vr[c][t] = *reinterpret_cast<const uint16_t*>(p + d0 / 2);
         else vr[c][t] = load_words<VB>(p + d0 * EB);
       }
     }
@@ -860,7 +860,24 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     if (last) {  // workgroup-uniform
       if (tid == 0)
         __hip_atomic_store(a.count + g0 * kCounterStride, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      // (The fence takes 4 us where all workgroups join at once. Of 4 bits up to
+      // eight parts are read as agent-scope atomics of 8 bytes instead: 32
+      // sequences of 2048 27.3 -> 23.7 us. With 32 parts those lose, 18.4 -> 20.6.)
+      auto join = [&](auto atomics) {
+      constexpr bool kAtomics = decltype(atomics)::value;
+      if constexpr (!kAtomics) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      auto one = [&](const float* p) {
+        if constexpr (kAtomics) return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        else return *p;
+      };
+      auto four = [&](const float* p) {
+        if constexpr (!kAtomics) return *reinterpret_cast<const f32x4*>(p);
+        const uint64_t* w = reinterpret_cast<const uint64_t*>(p);
+        const uint64_t lo = __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint64_t hi = __hip_atomic_load(w + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return __builtin_bit_cast(f32x4, u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                                               static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)});
+      };
       const float* p_first = a.part + (2 * g0 + second) * part_size;
       const float* p_rest = a.part + 2 * g0 * part_size;  // part i > 0 is p_step * i on
       const int64_t p_step = 2 * per_seq * part_size;
@@ -874,21 +891,21 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       f32x4 ahead[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
-        ahead[k] = reinterpret_cast<const f32x4*>(part(min(team + k * teams, parts - 1)))[min(tid / teams, quads - 1)];
+        ahead[k] = four(part(min(team + k * teams, parts - 1)) + min(tid / teams, quads - 1) * 4);
       // The parts' factors exp(m - max m) / sum, [head][part], in LDS.
       for (int r = wave; r < heads; r += kWaves) {
         const float* ml = part(min(lane, parts - 1)) + heads * DP + r;
-        const float m0 = lane < parts ? ml[0] : -INFINITY, l0 = ml[heads];
+        const float m0 = lane < parts ? one(ml) : -INFINITY, l0 = one(ml + heads);
         float top = m0;
-        for (int i = lane + kWave; i < parts; i += kWave) top = fmaxf(top, part(i)[heads * DP + r]);
+        for (int i = lane + kWave; i < parts; i += kWave) top = fmaxf(top, one(part(i) + heads * DP + r));
         top = wave_max(top);
         const float base = top == -INFINITY ? 0.f : top;
         float sum = 0.f;
         for (int i = lane; i < parts; i += kWave) {
           const float* p = part(i) + heads * DP + r;
-          const float f = exp2_fast((i < kWave ? m0 : p[0]) - base);
+          const float f = exp2_fast((i < kWave ? m0 : one(p)) - base);
           lds[r * parts + i] = f;
-          sum += f * (i < kWave ? l0 : p[heads]);
+          sum += f * (i < kWave ? l0 : one(p + heads));
         }
         sum = wave_sum(sum);
         const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
@@ -908,7 +925,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
           }
 #pragma unroll 8
           for (; i < parts; i += teams)
-            x += lds[r * parts + i] * reinterpret_cast<const f32x4*>(part(i))[q];
+            x += lds[r * parts + i] * four(part(i) + q * 4);
         }
         if (teams > 1) {
           sums[tid] = x;
@@ -922,6 +939,13 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
           for (int i = 0; i < 4; ++i)
             store_from_f32(a.out + row_at(r, a.out_row, a.out_head), IO, d + i, x[i]);
         }
+      }
+      };
+      if constexpr (F4) {
+        if (parts <= 8) join(std::true_type{});
+        else join(std::false_type{});
+      } else {
+        join(std::false_type{});
       }
     }
   }
@@ -964,7 +988,7 @@ Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t
   const int dp = decode_dim_pad(static_cast<int>(kv.dim));
   const bool apart = dp == 128 && kv.dtype != kE2M1 && kv.k_stride[3] != kv.dim && kv.page > 1;
   const int64_t room = 256 * (apart ? 1 : groups_per_cu(kv.dtype, dp));
-  p.shared = steps > (kv.dtype == kE2M1 ? 1 : 3) && seqs * p.per_seq < 3 * room && p.per_seq <= room && seqs * steps < (1 << 30);
+  p.shared = steps > 3 && seqs * p.per_seq < 3 * room && p.per_seq <= room && seqs * steps < (1 << 30);
   p.ranges = p.shared ? std::min(room / p.per_seq, seqs * steps) : seqs;
   return p;
 }

@@ -45,6 +45,8 @@ struct RopeArgs {
   float k_scale, v_scale;
   ExpView exps;
   FastDiv quarters;                  // dim / 4
+  double k_inv, v_inv;               // 1 / k_scale, 1 / v_scale
+  int q_blocks, kv_block, kv_parts;  // workgroups of q; tokens of one of k and v, and those that share them
 };
 
 __device__ __forceinline__ void sin_cos(double angle, float* s, float* c) {
@@ -239,143 +241,283 @@ __device__ __forceinline__ int lane8_max(int v) {
   return max(v, dpp<kDppRowHalfMirror>(v));
 }
 
-// The append to a cache of 4 bits. A thread takes four elements of k or v (or
-// eight of q), 8 threads next to each other a block of 32, whose power of two
-// they agree on. A code depends on the side of a border that its value lies
-// on, so k is turned, and k and v divided, in f64: the codes are those of the
-// exact values, up to a value within 2^-50 of a border. (A partner element is
-// loaded by both threads that need it; the second load is a cache hit.)
-template <bool VEC>
-__global__ __launch_bounds__(kThreads) void rope_append4_kernel(RopeArgs a) {
-  extern __shared__ double trig64[];  // [token][half] cosines, then sines
-  const int tid = threadIdx.x;
-  const int t0 = (blockIdx.x / a.head_blocks) * a.per_block, hb = blockIdx.x % a.head_blocks;
-  const int tokens = min(a.per_block, a.tokens - t0);
-  double* sines = trig64 + a.per_block * a.half;
-  for (int i = tid; i < tokens * a.half; i += kThreads) {
-    const int t = i / a.half, pair = i - t * a.half;
-    const int axis = (pair >= a.bound[0]) + (pair >= a.bound[1]) + (pair >= a.bound[2]);
-    sin_cos(a.pos[axis * a.pos_stride + t0 + t] * a.freq[pair], &sines[i], &trig64[i]);
-  }
-  __syncthreads();
+// |x| as f32, cut off with its last bit set where that loses anything: on the
+// same side of every border between two codes, and never on one that x is not
+// on. Below f32's normal numbers 0, above them the largest.
+__device__ __forceinline__ float cut_to_f32(double x) {
+  const uint32_t hi = static_cast<uint32_t>(__double2hiint(x)) & 0x7fffffffu, lo = static_cast<uint32_t>(__double2loint(x));
+  const uint32_t bits = __builtin_amdgcn_alignbit(hi, lo, 29) - (896u << 23) | min(lo & 0x1fffffffu, 1u);
+  const uint32_t small = hi < 0x38100000u ? 0u : bits;
+  return __builtin_bit_cast(float, hi >= 0x47f00000u ? 0x7f7fffffu : small);
+}
 
-  const int all = a.heads + 2 * a.kv_heads;
-  const int h0 = static_cast<int>(static_cast<int64_t>(all) * hb / a.head_blocks);
-  const int h1 = static_cast<int>(static_cast<int64_t>(all) * (hb + 1) / a.head_blocks);
-  // q, as in rope_kernel.
-  const int q_heads = max(0, min(h1, a.heads) - h0);
-  const int per_token = q_heads * static_cast<int>(a.items.d);
-  for (int i = tid; i < tokens * per_token; i += kThreads) {
-    const int t = i / per_token, j = i - t * per_token;
-    const int hi = div_by(j, a.items);
-    const int piece = j - hi * a.items.d;
-    const int64_t token = t0 + t;
-    const uint8_t* src = a.src[0] + token * a.row[0] + (h0 + hi) * a.head[0];
-    uint8_t* dst = a.out + token * a.out_row + (h0 + hi) * a.out_head;
-    const bool turns = piece * 4 < a.half, split = turns && !a.adjacent;
-    const int at0 = split ? piece * 4 : piece * 8, at1 = split ? a.half + piece * 4 : piece * 8 + 4;
-    f32x4 x = load4<VEC>(src, a.x_type, at0), y = load4<VEC>(src, a.x_type, at1);
-    if (turns) {
-      float c[4], s[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        c[e] = static_cast<float>(trig64[t * a.half + piece * 4 + e]);
-        s[e] = static_cast<float>(sines[t * a.half + piece * 4 + e]);
-      }
-      const f32x4 u = x, w = y;
-      if (split) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = u[e] * c[e] - w[e] * s[e];
-          y[e] = u[e] * s[e] + w[e] * c[e];
-        }
-      } else {
-        x = f32x4{u.x * c[0] - u.y * s[0], u.x * s[0] + u.y * c[0],
-                  u.z * c[1] - u.w * s[1], u.z * s[1] + u.w * c[1]};
-        y = f32x4{w.x * c[2] - w.y * s[2], w.x * s[2] + w.y * c[2],
-                  w.z * c[3] - w.w * s[3], w.z * s[3] + w.w * c[3]};
-      }
-    }
-    store4<VEC>(dst, a.out_type, at0, x);
-    store4<VEC>(dst, a.out_type, at1, y);
-  }
-
-  // k and v. 8 | dim / 4, so the 8 threads of a block are in one wave's row
-  // and take every turn of the loop together.
-  const int kv0 = max(0, h0 - a.heads), kv_here = max(0, h1 - a.heads) - kv0;
-  const int quarters = a.quarters.d, per = kv_here * quarters;
-  for (int i = tid; i < tokens * per; i += kThreads) {
-    const int t = i / per, j = i - t * per;
-    const int hi = div_by(j, a.quarters), at = (j - hi * quarters) * 4;
-    const bool is_v = kv0 + hi >= a.kv_heads;
-    const int head = kv0 + hi - (is_v ? a.kv_heads : 0);
-    const int64_t token = t0 + t;
-    const int64_t slot = a.slots[token];
-    if (slot < 0 || slot >= a.cache_slots) continue;
-    const uint8_t* src = is_v ? a.src[2] + token * a.row[2] + head * a.head[2]
-                              : a.src[1] + token * a.row[1] + head * a.head[1];
-    const f32x4 own = load4<VEC>(src, a.x_type, at);
-    double x[4] = {own.x, own.y, own.z, own.w};
-    if (!is_v && at < 2 * a.half) {
-      const double* c = trig64 + t * a.half;
-      const double* s = sines + t * a.half;
-      if (a.adjacent) {
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const int pair = (at + e) / 2;
-          const double u = x[e], w = x[e + 1];
-          x[e] = u * c[pair] - w * s[pair];
-          x[e + 1] = u * s[pair] + w * c[pair];
-        }
-      } else {
-        // The second half's elements turn by the sine as they are, the first
-        // half's by its negative.
-        const bool second = at >= a.half;
-        const int first = second ? at - a.half : at;
-        const f32x4 other = load4<VEC>(src, a.x_type, second ? first : at + a.half);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const double turn = s[first + e] * static_cast<double>(other[e]);
-          x[e] = x[e] * c[first + e] + (second ? turn : -turn);
-        }
-      }
-    }
-    const float scale = is_v ? a.v_scale : a.k_scale;
-    if (scale != 1.f) {
-      // The quotient with one correction: where x / scale is a number of f64,
-      // a border between two codes say, that number.
-      const double d = scale, r = 1.0 / d;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const double q = x[e] * r, rest = fma(-q, d, x[e]);
-        x[e] = fabs(q) < INFINITY ? copysign(fma(rest, r, q), q) : q;  // (-0 + 0 would be 0)
-      }
-    }
-    // The largest |x| by its upper word: m * 2^E is below 7 * 2^e from e = E - 2
-    // on where m < 1.75, else from E - 1 on.
+// Four elements to their codes (16 bits) and, in `power`, the exponent of the
+// block that 8 threads next to each other have, or NaN's. A code depends on the
+// side of a border that its value lies on, so the quotient by the scale is f64's:
+// with one correction it is the number itself where that is one of f64, a border
+// between two codes say.
+__device__ __forceinline__ uint32_t codes_of(const double (&x)[4], float scale, double inverse, int* power) {
+  double y[4] = {x[0], x[1], x[2], x[3]};
+  auto largest = [&]() {
     int top = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, static_cast<int>(__double2hiint(x[e]) & 0x7fffffff));
-    top = lane8_max(top);
-    const bool nan = top > 0x7ff00000;
-    const int power = min(max((top >> 20) - 1023 - 2 + ((top >> 18 & 3) == 3), -23), 13);
-    const double down = __hiloint2double((1023 - power) << 20, 0);
-    uint32_t codes = 0;
+    for (int e = 0; e < 4; ++e) top = max(top, static_cast<int>(__double2hiint(y[e]) & 0x7fffffff));
+    return lane8_max(top);
+  };
+  int top;
+  if (scale != 1.f) {
+    const double d = scale;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const double u = fabs(x[e]) * down;
-      const uint32_t code = (u > 0.25) + (u >= 0.75) + (u > 1.25) + (u >= 1.75) + (u > 2.5) + (u >= 3.5) + (u > 5.0);
-      codes |= (code | (__double2hiint(x[e]) < 0 ? 8u : 0u)) << (4 * e);
+      const double q = x[e] * inverse;
+      y[e] = fma(fma(-q, d, x[e]), inverse, q);
     }
+    top = largest();
+    if (__ballot(top >= 0x7ff00000)) {
+      // (An infinity's correction is NaN.)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = fabs(x[e]) < INFINITY ? y[e] : x[e];
+      top = largest();
+    }
+  } else {
+    top = largest();
+  }
+  // The largest |y| by its upper word: m * 2^E is below 7 * 2^e from e = E - 2 on
+  // where m < 1.75, else from E - 1 on.
+  const int e = min(max((top >> 20) - 1023 - 2 + ((top >> 18 & 3) == 3), -23), 13) + 127;
+  *power = top > 0x7ff00000 ? 255 : e;
+  float u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = copysignf(cut_to_f32(y[i]), __builtin_bit_cast(float, __double2hiint(x[i])));
+  const uint32_t low = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, u[0], u[1], block_power(e), 0);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(low, u[2], u[3], block_power(e), 1);
+}
+
+// Eight elements: as they lie in memory, and as f32.
+struct Raw8 {
+  u32x4 a, b;  // b: of f32
+};
+__device__ __forceinline__ Raw8 load8(const uint8_t* p, int type, int at) {
+  Raw8 r;
+  r.a = *reinterpret_cast<const u32x4*>(p + at * (type == kF32 ? 4 : 2));
+  r.b = u32x4{0, 0, 0, 0};
+  if (type == kF32) r.b = *reinterpret_cast<const u32x4*>(p + at * 4 + 16);
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Raw8& r, int type, float (&x)[8]) {
+  if (type == kF32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t u = r.a[e], w = r.b[e];
+      x[e] = __builtin_bit_cast(float, u);
+      x[4 + e] = __builtin_bit_cast(float, w);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f32x2 y = type == kBF16 ? unpack2<kBF16>(r.a[e]) : unpack2<kF16>(r.a[e]);
+      x[2 * e] = y.x;
+      x[2 * e + 1] = y.y;
+    }
+  }
+}
+__device__ __forceinline__ void store8(uint8_t* p, int type, int at, const float (&x)[8]) {
+  if (type == kF32) {
+    *reinterpret_cast<f32x4*>(p + at * 4) = f32x4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4*>(p + at * 4 + 16) = f32x4{x[4], x[5], x[6], x[7]};
+  } else if (type == kBF16) {
+    *reinterpret_cast<u32x4*>(p + at * 2) = u32x4{pack2<kBF16>(x[0], x[1]), pack2<kBF16>(x[2], x[3]),
+                                                  pack2<kBF16>(x[4], x[5]), pack2<kBF16>(x[6], x[7])};
+  } else {
+    *reinterpret_cast<u32x4*>(p + at * 2) = u32x4{pack2<kF16>(x[0], x[1]), pack2<kF16>(x[2], x[3]),
+                                                  pack2<kF16>(x[4], x[5]), pack2<kF16>(x[6], x[7])};
+  }
+}
+
+// The append to a cache of 4 bits. The first workgroups turn q, as rope_kernel
+// does (WIDE: 16 elements a thread, in 16-byte words). The others have some tokens' k and v each: a thread takes four elements,
+// 8 threads next to each other a block of 32, whose power of two they agree on. k
+// is turned in f64: the codes are those of the exact values, up to a value within
+// 2^-50 of a border. (A partner element is loaded by both threads that need it;
+// the second load is a cache hit.)
+//
+// Measured: 8192 tokens (32 + 2 x 8 heads of 128, bf16, three axes, both scales not
+// 1) 63 us, 2.8 TB/s, as the append to a bf16 cache; without k and v 44. What it
+// waits for is the chain from positions to angles to stores. (Codes by seven f64
+// comparisons each, a reciprocal in each thread and 8-byte words took 79.)
+template <bool VEC, bool WIDE>
+__global__ __launch_bounds__(kThreads) void rope_append4_kernel(RopeArgs a) {
+  extern __shared__ double trig64[];
+  const int tid = threadIdx.x;
+  auto axis_of = [&](int pair) { return (pair >= a.bound[0]) + (pair >= a.bound[1]) + (pair >= a.bound[2]); };
+  if (static_cast<int>(blockIdx.x) < a.q_blocks) {
+    float* trig = reinterpret_cast<float*>(trig64);  // [token][half] cosines, then sines
+    const int t0 = (blockIdx.x / a.head_blocks) * a.per_block, hb = blockIdx.x % a.head_blocks;
+    const int tokens = min(a.per_block, a.tokens - t0);
+    float* sines = trig + a.per_block * a.half;
+    const int h0 = static_cast<int>(static_cast<int64_t>(a.heads) * hb / a.head_blocks);
+    const int h1 = static_cast<int>(static_cast<int64_t>(a.heads) * (hb + 1) / a.head_blocks);
+    const uint8_t* q = a.src[0] + t0 * a.row[0] + h0 * a.head[0];
+    uint8_t* out = a.out + t0 * a.out_row + h0 * a.out_head;
+    const int per_token = (h1 - h0) * static_cast<int>(a.items.d), items = tokens * per_token;
+    // An item: 4 or 8 pairs of a head, or as many elements that are copied.
+    constexpr int PAIRS = WIDE ? 8 : 4;
+    struct Item {
+      int t, piece, at0, at1;
+      int64_t src, dst;
+      bool turns, split;
+    };
+    auto item = [&](int i) {
+      Item m;
+      m.t = a.per_block == 1 ? 0 : i / per_token;
+      const int j = i - m.t * per_token, hi = div_by(j, a.items);
+      m.piece = j - hi * a.items.d;
+      m.turns = m.piece * PAIRS < a.half;
+      m.split = m.turns && !a.adjacent;
+      m.at0 = m.piece * (m.split ? PAIRS : 2 * PAIRS);
+      m.at1 = m.split ? a.half + m.at0 : m.at0 + PAIRS;
+      m.src = m.t * a.row[0] + hi * a.head[0];
+      m.dst = m.t * a.out_row + hi * a.out_head;
+      return m;
+    };
+    Raw8 x0, x1;
+    if constexpr (WIDE) {
+      // The first item's loads are under way while the angles are worked out.
+      const Item m = item(min(tid, items - 1));
+      x0 = load8(q + m.src, a.x_type, m.at0);
+      x1 = load8(q + m.src, a.x_type, m.at1);
+    }
+    for (int i = tid; i < tokens * a.half; i += kThreads) {
+      const int t = i / a.half, pair = i - t * a.half;
+      sin_cos(a.pos[axis_of(pair) * a.pos_stride + t0 + t] * a.freq[pair], &sines[i], &trig[i]);
+    }
+    __syncthreads();
+    for (int i = tid; i < items; i += kThreads) {
+      const Item m = item(i);
+      float u[PAIRS], w[PAIRS];
+      if constexpr (WIDE) {
+        if (i != tid) {
+          x0 = load8(q + m.src, a.x_type, m.at0);
+          x1 = load8(q + m.src, a.x_type, m.at1);
+        }
+        unpack8(x0, a.x_type, u);
+        unpack8(x1, a.x_type, w);
+      } else {
+        const f32x4 y = load4<VEC>(q + m.src, a.x_type, m.at0), z = load4<VEC>(q + m.src, a.x_type, m.at1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = y[e], w[e] = z[e];
+      }
+      if (m.turns) {
+        const float* c = trig + m.t * a.half + m.piece * PAIRS;
+        const float* s = sines + m.t * a.half + m.piece * PAIRS;
+        if (m.split) {
+#pragma unroll
+          for (int e = 0; e < PAIRS; ++e) {
+            const float x = u[e], y = w[e];
+            u[e] = x * c[e] - y * s[e];
+            w[e] = x * s[e] + y * c[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < PAIRS; e += 2) {
+            const float x = u[e], y = u[e + 1], z = w[e], v = w[e + 1];
+            const int p = e / 2, r = PAIRS / 2 + e / 2;
+            u[e] = x * c[p] - y * s[p];
+            u[e + 1] = x * s[p] + y * c[p];
+            w[e] = z * c[r] - v * s[r];
+            w[e + 1] = z * s[r] + v * c[r];
+          }
+        }
+      }
+      if constexpr (WIDE) {
+        store8(out + m.dst, a.out_type, m.at0, u);
+        store8(out + m.dst, a.out_type, m.at1, w);
+      } else {
+        store4<VEC>(out + m.dst, a.out_type, m.at0, f32x4{u[0], u[1], u[2], u[3]});
+        store4<VEC>(out + m.dst, a.out_type, m.at1, f32x4{w[0], w[1], w[2], w[3]});
+      }
+    }
+    return;
+  }
+
+  const int block = blockIdx.x - a.q_blocks;
+  const int t0 = block / a.kv_parts * a.kv_block, part = block % a.kv_parts;
+  const int tokens = min(a.kv_block, a.tokens - t0);
+  double* sines = trig64 + a.kv_block * a.half;
+  for (int i = tid; i < tokens * a.half; i += kThreads) {
+    const int t = i / a.half, pair = i - t * a.half;
+    sin_cos(a.pos[axis_of(pair) * a.pos_stride + t0 + t] * a.freq[pair], &sines[i], &trig64[i]);
+  }
+  __syncthreads();
+  const int h0 = static_cast<int>(static_cast<int64_t>(a.kv_heads) * part / a.kv_parts);
+  const int h1 = static_cast<int>(static_cast<int64_t>(a.kv_heads) * (part + 1) / a.kv_parts);
+  // 8 | dim / 4: the 8 threads of a block are in one wave's row and take every
+  // turn of a loop together.
+  const int quarters = a.quarters.d, items = (h1 - h0) * quarters;
+  // A thread's four elements of k, those that k's turn needs besides, and of v.
+  struct Own {
+    f32x4 k, other, v;
+  };
+  auto load = [&](int t, int i) {
+    const int64_t token = t0 + t;
+    const int head = div_by(i, a.quarters), at = (i - head * quarters) * 4;
+    const uint8_t* k = a.src[1] + token * a.row[1] + (h0 + head) * a.head[1];
+    Own o;
+    o.k = load4<VEC>(k, a.x_type, at);
+    o.v = load4<VEC>(a.src[2] + token * a.row[2] + (h0 + head) * a.head[2], a.x_type, at);
+    o.other = o.k;
+    if (!a.adjacent && at < 2 * a.half) o.other = load4<VEC>(k, a.x_type, at >= a.half ? at - a.half : at + a.half);
+    return o;
+  };
+  // The next token's elements load while one's are worked on.
+  Own next = load(0, min(tid, items - 1));
+  for (int t = 0; t < tokens; ++t) {
+    Own now = next;
+    next = load(min(t + 1, tokens - 1), min(tid, items - 1));
+    const int64_t slot = a.slots[t0 + t];
+    if (slot < 0 || slot >= a.cache_slots) continue;  // workgroup-uniform
     const uint32_t page = div_by(static_cast<uint32_t>(slot), a.kv.page);
     const int64_t in = slot - static_cast<int64_t>(page) * a.kv.page.d;
-    uint8_t* row = is_v ? a.kv.v + page * a.kv.v_page + head * a.kv.v_head + in * a.kv.v_tok
-                        : a.kv.k + page * a.kv.k_page + head * a.kv.k_head + in * a.kv.k_tok;
-    *reinterpret_cast<uint16_t*>(row + at / 2) = static_cast<uint16_t>(codes);
-    if (at % 32 == 0) {
-      uint8_t* exps = is_v ? a.exps.v + page * a.exps.v_page + head * a.exps.v_head + in * a.exps.v_tok
-                           : a.exps.k + page * a.exps.k_page + head * a.exps.k_head + in * a.exps.k_tok;
-      exps[at / 32] = static_cast<uint8_t>(nan ? 255 : power + 127);
+    uint8_t* k_at = a.kv.k + page * a.kv.k_page + in * a.kv.k_tok + h0 * a.kv.k_head;
+    uint8_t* v_at = a.kv.v + page * a.kv.v_page + in * a.kv.v_tok + h0 * a.kv.v_head;
+    uint8_t* ke_at = a.exps.k + page * a.exps.k_page + in * a.exps.k_tok + h0 * a.exps.k_head;
+    uint8_t* ve_at = a.exps.v + page * a.exps.v_page + in * a.exps.v_tok + h0 * a.exps.v_head;
+    const double* c = trig64 + t * a.half;
+    const double* s = sines + t * a.half;
+    for (int i = tid; i < items; i += kThreads) {
+      if (i != tid) now = load(t, i);
+      const int head = div_by(i, a.quarters), at = (i - head * quarters) * 4;
+      const f32x4 own = now.k, other = now.other, v = now.v;
+      double x[4] = {own.x, own.y, own.z, own.w};
+      if (at < 2 * a.half) {
+        if (a.adjacent) {
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const int pair = (at + e) / 2;
+            const double u = x[e], w = x[e + 1];
+            x[e] = u * c[pair] - w * s[pair];
+            x[e + 1] = u * s[pair] + w * c[pair];
+          }
+        } else {
+          // The second half's elements turn by the sine as they are, the first
+          // half's by its negative.
+          const bool second = at >= a.half;
+          const int first = second ? at - a.half : at;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const double turn = s[first + e] * static_cast<double>(other[e]);
+            x[e] = x[e] * c[first + e] + (second ? turn : -turn);
+          }
+        }
+      }
+      int power;
+      const uint32_t codes = codes_of(x, a.k_scale, a.k_inv, &power);
+      *reinterpret_cast<uint16_t*>(k_at + head * a.kv.k_head + at / 2) = static_cast<uint16_t>(codes);
+      if (at % 32 == 0) ke_at[head * a.exps.k_head + at / 32] = static_cast<uint8_t>(power);
+      const double w[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t v_codes = codes_of(w, a.v_scale, a.v_inv, &power);
+      *reinterpret_cast<uint16_t*>(v_at + head * a.kv.v_head + at / 2) = static_cast<uint16_t>(v_codes);
+      if (at % 32 == 0) ve_at[head * a.exps.v_head + at / 32] = static_cast<uint8_t>(power);
     }
   }
 }
@@ -385,6 +527,40 @@ __global__ __launch_bounds__(kThreads) void rope_append4_kernel(RopeArgs a) {
 bool rows_aligned(const RowsView& r) {
   const uintptr_t w = static_cast<uintptr_t>(4 * elem_bytes(r.type));
   return reinterpret_cast<uintptr_t>(r.data) % w == 0 && r.row % 4 == 0 && r.head % 4 == 0;
+}
+
+// Launches of whole tokens whose threads 32 bits count.
+hipError_t launch_append4(RopeArgs a, bool vec, bool wide, int64_t tokens, int64_t heads, hipStream_t stream) {
+  const int64_t most = int64_t{1} << 21;
+  if (wide) a.items = fast_div(static_cast<uint32_t>(a.dim / 16));
+  const int64_t q_items = heads * a.items.d, kv_items = static_cast<int64_t>(a.kv_heads) * a.quarters.d;
+  for (int64_t left = tokens; left > 0; left -= most) {
+    const int64_t now = std::min(left, most);
+    a.tokens = static_cast<int>(now);
+    a.per_block = now >= 1024 && q_items < kThreads ? static_cast<int>(std::min<int64_t>(kMaxTokens, kThreads / q_items)) : 1;
+    const int64_t q_groups = (now + a.per_block - 1) / a.per_block;
+    a.head_blocks = static_cast<int>(std::clamp<int64_t>(1024 / q_groups, 1, std::min<int64_t>(heads, (q_items + kThreads - 1) / kThreads)));
+    // Four tokens' sines and cosines keep all threads busy; few tokens are
+    // shared by workgroups instead.
+    a.kv_block = now >= 4096 ? kMaxTokens : 1;
+    const int64_t kv_groups = (now + a.kv_block - 1) / a.kv_block;
+    a.kv_parts = static_cast<int>(std::clamp<int64_t>(1024 / kv_groups, 1, std::min<int64_t>(a.kv_heads, (kv_items + kThreads - 1) / kThreads)));
+    a.q_blocks = static_cast<int>(q_groups * a.head_blocks);
+    const size_t lds = std::max<size_t>(a.per_block * sizeof(float), a.kv_block * sizeof(double)) * a.half * 2;
+    const dim3 grid(static_cast<uint32_t>(a.q_blocks + kv_groups * a.kv_parts));
+    if (wide)
+      rope_append4_kernel<true, true><<<grid, dim3(kThreads), lds, stream>>>(a);
+    else if (vec)
+      rope_append4_kernel<true, false><<<grid, dim3(kThreads), lds, stream>>>(a);
+    else
+      rope_append4_kernel<false, false><<<grid, dim3(kThreads), lds, stream>>>(a);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    for (int i = 0; i < 3; ++i) a.src[i] += now * a.row[i];
+    a.out += now * a.out_row;
+    a.pos += now;
+    a.slots += now;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
@@ -419,6 +595,8 @@ hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k
     a.cache_slots = kv->pages * kv->page;
     a.k_scale = kv->k_scale;
     a.v_scale = kv->v_scale;
+    a.k_inv = 1.0 / kv->k_scale;
+    a.v_inv = 1.0 / kv->v_scale;
     a.slots = slots;
   }
   a.pos = pos;
@@ -451,7 +629,15 @@ hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k
     ++a.per_block;
   const int64_t blocks = (tokens + a.per_block - 1) / a.per_block;
   a.head_blocks = static_cast<int>(std::clamp<int64_t>(1024 / blocks, 1, (items + kThreads - 1) / kThreads));
-  const size_t lds = static_cast<size_t>(a.per_block) * a.half * 2 * (four ? sizeof(double) : sizeof(float));
+  if (four) {
+    // q and its output in 16-byte words of eight 16-bit elements: their rows lie
+    // so, and a half of the pairs is a multiple of eight.
+    auto words = [](const RowsView& r) {
+      return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && r.row % 8 == 0 && r.head % 8 == 0;
+    };
+    return launch_append4(a, vec, vec && a.half % 8 == 0 && words(q) && words(out), tokens, heads, stream);
+  }
+  const size_t lds = static_cast<size_t>(a.per_block) * a.half * 2 * sizeof(float);
   // A launch's threads are counted in 32 bits, and more wrap round without an
   // error: so many workgroups (of 2^24 - 1) take the tokens in several launches.
   const int64_t most = int64_t{1} << 23;
@@ -459,11 +645,7 @@ hipError_t launch_rope(const RowsView& out, const RowsView& q, const RowsView* k
     const int64_t now = std::min(left, most), done = now * a.per_block;
     a.tokens = static_cast<int>(std::min(done, tokens));
     const dim3 grid(static_cast<uint32_t>(now * a.head_blocks));
-    if (four && vec)
-      rope_append4_kernel<true><<<grid, dim3(kThreads), lds, stream>>>(a);
-    else if (four)
-      rope_append4_kernel<false><<<grid, dim3(kThreads), lds, stream>>>(a);
-    else if (vec)
+    if (vec)
       rope_kernel<true><<<grid, dim3(kThreads), lds, stream>>>(a);
     else
       rope_kernel<false><<<grid, dim3(kThreads), lds, stream>>>(a);
