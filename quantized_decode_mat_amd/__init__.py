@@ -38,6 +38,7 @@ EXPORTS = (
     "xq_gemm_q4k_id_workspace_bytes", "xq_gemm_q4k_small_m_noalloc",
     "xq_attn_decode", "xq_attn_decode_workspace_bytes", "xq_attn_prefill", "xq_rope", "xq_rope_append",
     "xq_cache_copy", "xq_cache_free", "xq_cache_fork", "xq_cache_compact", "xq_cache_workspace_bytes",
+    "xq_cache_read", "xq_moe_route", "xq_moe_route_workspace_bytes", "xq_moe_q4k", "xq_moe_q4k_workspace_bytes",
 )
 XQ_NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024
 
