@@ -702,16 +702,21 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
   store_from_f32(a.y + token * a.y_row, a.type, row, sum);
 }
 
+// The same bound from every call, so that calls of several threads do not lower
+// one another's.
+constexpr int kMostLds = 80 * 1024;
+template <class Kernel>
+hipError_t allow_lds(Kernel kernel, size_t lds) {
+  if (lds <= 48 * 1024) return hipSuccess;
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
+}
+
 template <int NT, int LPR>
 hipError_t launch_up(MoeArgs a, hipStream_t stream) {
   constexpr int W = 4, R = up_rows(NT, LPR);
-  const size_t lds = static_cast<size_t>(NT) * a.nb * kQ8KBytes;
+  const size_t lds = static_cast<size_t>(NT) * a.nb * kQ8KBytes;  // (2 x 128 blocks at most)
   auto kernel = moe_up_kernel<NT, LPR, W>;
-  if (lds > 48 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
-    if (e != hipSuccess) return e;
-  }
+  if (const hipError_t e = allow_lds(kernel, lds); e != hipSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(a.tokens) * a.used;
   // So many groups a wave that all workgroups are on the card at once.
   constexpr int64_t kRoom = 256 * 3;
@@ -750,11 +755,7 @@ template <int PF>
 hipError_t launch_down(MoeArgs a, hipStream_t stream) {
   const size_t lds = static_cast<size_t>(a.used) * a.nb * kQ8KBytes;
   auto kernel = moe_down_kernel<kDownWaves, PF>;
-  if (lds > 48 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
-    if (e != hipSuccess) return e;
-  }
+  if (const hipError_t e = allow_lds(kernel, lds); e != hipSuccess) return e;
   // So many rows a wave that all workgroups are on the card at once, one a CU.
   const int per_token = std::max(1, 256 / a.tokens);
   a.groups = (a.rows + per_token * kDownWaves - 1) / (per_token * kDownWaves);
@@ -766,7 +767,7 @@ hipError_t launch_down(MoeArgs a, hipStream_t stream) {
 // Mat-vecs, and down token by token, where tokens hardly share experts (as many
 // experts as pairs and more) and a token's h fits a workgroup's LDS.
 bool by_rows(int64_t tokens, int64_t used, int64_t experts, int64_t ffn) {
-  return (tokens == 1 || tokens * used <= experts) && used * (ffn / 256) * kQ8KBytes <= 80 * 1024;
+  return (tokens == 1 || tokens * used <= experts) && used * (ffn / 256) * kQ8KBytes <= kMostLds;
 }
 
 struct Layout {

@@ -140,6 +140,12 @@ LAYERS = [
     (512, 1, 3, 256, 256, "f32"),
     (16, 8, 128, 768, 256, "bf16"),
     (64, 8, 128, 256, 512, "f16"),
+    (1, 1, 2, 32768, 256, "bf16"),      # the widest, every way
+    (2, 2, 5, 32768, 256, "f32"),
+    (1, 2, 2, 256, 32768, "f16"),
+    (3, 1, 2, 256, 32768, "f32"),
+    (5, 1, 2, 32768, 512, "bf16"),
+    (1, 512, 1024, 256, 256, "f32"),    # all 512 slots a token's
 ]
 
 
@@ -217,6 +223,28 @@ def test_layer_in_a_graph_on_another_stream():
             assert torch.equal(s["y"], want)
 
 
+def test_two_layers_at_once():
+    """Two streams, each with its own workspace, and x of one in both."""
+    g = torch.Generator(device=DEV).manual_seed(6)
+    runs = []
+    for tokens, experts in ((1, 8), (3, 40), (24, 8)):
+        c = dict(tokens=tokens, used=4, experts=experts, hidden=1024, ffn=768, io="bf16")
+        a = state(c, 7)
+        b = dict(a, ids=torch.randint(0, experts, (tokens, 4), device=DEV, generator=g, dtype=torch.int32),
+                 full=a["full"].clone(), ws=torch.zeros_like(a["ws"]))
+        b["y"] = b["full"][:, :1024]
+        runs.append((c, a, b))
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for c, a, b in runs:
+            run(c, a, stream=one)
+            run(c, b, stream=two)
+    for c, a, b in runs:
+        check(c, a)
+        check(c, b)
+
+
 # ---------------------------------------------------------------- router
 
 ROUTES = [
@@ -229,6 +257,8 @@ ROUTES = [
     (64, 200, 64, 1000, "f16", "f16", "sigmoid", False, True),
     (9, 1024, 32, 520, "bf16", "bf16", "softmax", True, True),
     (512, 8, 2, 256, "f32", "f32", "softmax", False, True),
+    (512, 1024, 64, 8, "f32", "bf16", "sigmoid", True, True),
+    (2, 6, 2, 1048576, "f32", "f32", "softmax", False, True),
 ]
 
 
