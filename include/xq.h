@@ -378,7 +378,9 @@ enum { XQ_F32 = 0, XQ_BF16 = 1, XQ_F16 = 2, XQ_E4M3 = 3, XQ_E2M1 = 4 };
  *  stores powers 2^-23 .. 2^13 (bytes 104..140), which every call reads exactly,
  *  and 255 for a block that holds a NaN, all of which then are NaN. Of other
  *  bytes those up to 250 are read as what they stand for, but in a chunk's
- *  attention with XQ_F16 as f16 holds it. Other types do not read these fields.
+ *  attention with XQ_F16 as f16 holds it. (Attention's sums are f32's, as with
+ *  every type: a row's |q||k| added up over its dims, and the |v| of the tokens
+ *  that it sees, have to stay below 2^127.) Other types do not read these fields.
  *  1 <= layers <= 2^24; 1 <= pages, page; 1 <= kv_heads <= 2^20; pages * page <= 2^31 - 1 (a slot is an
  *  int32's worth; byte offsets are 64-bit). dim a multiple of 16, 16..256.
  *  k and v 16-byte aligned; strides >= 0 and multiples of 16 bytes.

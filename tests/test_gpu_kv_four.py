@@ -280,17 +280,34 @@ def test_decode_nan_that_is_seen():
     assert s["out"][0, :2].isnan().all() and s["out"][0, 2:].isfinite().all() and s["out"][1].isfinite().all()
 
 
-@pytest.mark.parametrize("low,high", [(104, 112), (132, 140), (2, 4), (246, 250)])
+@pytest.mark.parametrize("low,high", [(104, 112), (132, 140), (2, 4), (237, 241)])
 def test_powers_at_the_ends(low, high):
-    """The smallest and largest powers that the append stores, and those that are read beside them."""
+    """The smallest and largest powers that the append stores, and those that are read beside them: 700 tokens of up to
+    6 * 2^114 add up to less than 2^127."""
+    g = torch.Generator(device=DEV).manual_seed(2)
     s = setup([700], 4, 2, 128, 16, "f32", "hnd")
     for x in (s["k_exp"], s["v_exp"]):
-        x.copy_(torch.where(x == 255, x, torch.randint(low, high + 1, x.shape, device=DEV, dtype=torch.int32).to(torch.uint8)))
+        new = torch.randint(low, high + 1, x.shape, device=DEV, dtype=torch.int32, generator=g).to(torch.uint8)
+        x.copy_(torch.where(x == 255, x, new))
     # scores of a size that f32 holds
     s["scale"] = 2.0 ** min(100, 127 - high)
     s["q"] *= 0.05
     decode(s, 0, 0, 700)
     check_single(s, [700], 0, 0, "powers %d..%d" % (low, high))
+
+
+def test_read_of_all_powers():
+    g = torch.Generator(device=DEV).manual_seed(2)
+    k, k_exp = four.pool(16, 1, 16, 32, "hnd", g, DEV)
+    v, v_exp = four.pool(16, 1, 16, 32, "hnd", g, DEV)
+    byte = torch.arange(256, device=DEV).clamp(max=250).view(16, 1, 16).to(torch.uint8)
+    k_exp[..., 0], v_exp[..., 0] = byte, 250 - byte
+    got = [torch.empty(256, 1, 32, device=DEV) for _ in range(2)]
+    xq.xq_cache_read(got[0], got[1], four.cache(xq, k, k_exp, v, v_exp, (1.0, 1.0)), torch.arange(256, device=DEV))
+    for x, want in zip(got, (four.values(k, k_exp), four.values(v, v_exp))):
+        want = want.view(256, 1, 32)
+        normal = (want == 0) | (want.abs() >= 2.0 ** -126)
+        assert torch.equal(x.double()[normal], want[normal])
 
 
 def test_decode_past_32_bit_offsets():
