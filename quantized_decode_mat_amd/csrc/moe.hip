@@ -16,6 +16,14 @@
 // A row's dot is the mat-vec's (q4k_row.h): four lanes a super-block. Rows of
 // at most 8 or 4 blocks take a half or a quarter of a wave, which then holds
 // two or four rows, gate's and up's next to each other.
+//
+// Measured, router and experts together: one token, 8 of 64 experts, 2048 x 1536:
+// 21.6 us (43 MB; 5.9 at a streaming read's rate); five tokens, 6 of 64, 2048 x
+// 1280: 42.8 (110 MB, 15); 16 tokens, 2 of 8, 4096 x 14336: 205 us (785 MB, 108).
+//
+// Precision: the products are whole numbers up to the scales, sums over blocks
+// and slots f32. The activations go to q8_K twice, as the mat-vecs' do; h stays
+// f32 in between.
 #include <algorithm>
 
 #include "kv_device.h"
@@ -87,6 +95,12 @@ __device__ __forceinline__ Row8 load_x8(const uint8_t* row, int type, int at) {
   return r;
 }
 
+// What bounds it is latency: one read of the router's rows (0.3 to 8 MB), the sums
+// through LDS, an arrival, the ranking. Four experts a workgroup put 16 workgroups
+// on 64 experts, whose x stays in registers for all four; 512 threads cover 4096
+// columns at once. Measured: 64 experts of 2048 columns, one token 6.0 us, five
+// tokens 8.9.
+//
 // A workgroup has four experts' rows against NT tokens; its waves share the
 // columns, and LDS adds up their sums. The last workgroup of a tile of tokens to
 // arrive ranks them, a wave a token: the highest key `used` times over, the
@@ -247,6 +261,15 @@ __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 constexpr int up_steps(int nt) { return nt == 1 ? 4 : 2; }
 constexpr int up_rows(int nt, int lpr) { return up_steps(nt) * (kWave / lpr) / 2; }
 
+// What bounds it: the weights' bytes, and with 10 to 25 KB a wave in all the start
+// of that stream (ids, then the first weights; x is quantized meanwhile). Four
+// rows of weights in flight hide it for one pair; two where the pairs of a pass
+// take their registers. Nothing around the loads is conditional, so that the
+// compiler lets them pass the dots before them (five tokens' layer 68 -> 43 us with that, all
+// workgroups on the card at once, and reciprocals in place of divisions).
+// Measured: 8 pairs, 2 x 1536 rows of 2048 columns, 28 MB: 8.0 to 9.7 us; 30 pairs of
+// about 28 experts, 2 x 1280 rows, 73 MB: 25 us.
+//
 // Gate and up, and silu(gate) * up. NT: pairs of one pass. LPR: lanes of a row
 // (nb <= LPR / 4 where it is below 64). A workgroup has W waves, each `groups`
 // times R rows of h, of the expert of pair blockIdx.y.
@@ -385,6 +408,11 @@ __global__ __launch_bounds__(W * kWave, 3) void moe_up_kernel(MoeArgs a) {
 // after the other. The workgroup quantizes the token's h, used * nb blocks, while
 // its first weights load.
 // PF: steps of 16 blocks under way, all of a row's up to four.
+//
+// What bounds it: for one token the chain ids -> weights and h -> codes -> LDS ahead
+// of 14 MB; one row of all slots a wave keeps the sum over the slots in registers
+// (no h of a pair is read twice, no partial sums to add). Measured: 2048 rows of
+// 8 x 1536 columns, 14 MB: 8.2 us; five tokens, 6 x 1280: 14 us.
 template <int W, int PF>
 __global__ __launch_bounds__(W * kWave) void moe_down_kernel(MoeArgs a) {
   constexpr int QB = 3;     // blocks of a wave quantized side by side
@@ -494,6 +522,13 @@ __global__ __launch_bounds__(W * kWave) void moe_down_kernel(MoeArgs a) {
 // pairs by or-ing a 2^10 over them (1024 + q, or 1024 + 16 q) and one fused
 // multiply-add that takes it off again. The mins ride on a ninth instruction,
 // against sums of eight codes. The pairs' rows come packed in that order.
+//
+// What bounds it: bytes, read once an expert whatever its pairs, and next to them
+// the VALU work that widens a weight once per 16 pairs. (int8 instructions take
+// the codes without widening, but their sums need a scale per 32 columns: more
+// VALU work than this.) Measured, 16 tokens, 2 of 8 experts of 4096 x 14336: gate and
+// up 528 MB 125 to 135 us, 4.1 TB/s; down 264 MB 65 to 72 us; packing 2 x 4.8, the
+// sum over slots 4.7.
 
 constexpr int kPackHalves = 288;               // of a block: 256 codes, 32 sums of eight
 constexpr int kPackBytes = kPackHalves * 2;
@@ -509,7 +544,8 @@ constexpr int kRowBytes = kChunk * kQ4KBytes, kRowWords = kRowBytes / 16;
 constexpr int kRowPitch = kRowBytes + 16;      // 8 rows of 16-byte reads hit all banks
 constexpr int kRowLoads = (16 * kRowWords + kWave - 1) / kWave;
 
-// Rows of any type to packed blocks and their scales, a wave a block.
+// Rows of any type to packed blocks and their scales, a wave a block. (A launch:
+// 4.8 us for 16 rows of 4096 as for 32 of 14336.)
 __global__ __launch_bounds__(256) void moe_pack_kernel(uint8_t* packed, float* scales, const uint8_t* x, int64_t x_row,
                                                        int type, FastDiv nb, int blocks) {
   const int i = blockIdx.x * 4 + threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -689,7 +725,8 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void moe_tile_kernel(MoeArgs
   }
 }
 
-// y[t] = sum over its slots of weight * (down's row of the pair).
+// y[t] = sum over its slots of weight * (down's row of the pair), in the slots'
+// order whichever workgroup wrote them: no atomics. 16 x 4096 of 2 slots: 4.7 us.
 __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
   const int row = blockIdx.x * 256 + threadIdx.x, token = blockIdx.y;
   if (row >= a.rows) return;
@@ -765,7 +802,14 @@ hipError_t launch_down(MoeArgs a, hipStream_t stream) {
 }
 
 // Mat-vecs, and down token by token, where tokens hardly share experts (as many
-// experts as pairs and more) and a token's h fits a workgroup's LDS.
+// experts as pairs and more) and a token's h fits a workgroup's LDS (two
+// workgroups a CU). The experts' call alone, mat-vecs against tiles, us:
+//   8 experts, 4096 x 14336, 2 used: 1 token 55 / 86, 2 87 / 102, 3 123 / 133,
+//     4 160 / 142, 8 325 / 185
+//   64 experts, 2048 x 1536, 8 used: 1 token 16 / 29, 2 24 / 39
+//   64 experts, 2048 x 1280, 6 used: 5 tokens 32 / 55, 10 67 / 74, 16 91 / 91
+//   128 experts, 2048 x 768, 8 used: 16 tokens 81 / 90
+//   16 experts, 1024 x 1024, 4 used: 4 tokens 14 / 22, 8 20 / 26
 bool by_rows(int64_t tokens, int64_t used, int64_t experts, int64_t ffn) {
   return (tokens == 1 || tokens * used <= experts) && used * (ffn / 256) * kQ8KBytes <= kMostLds;
 }
