@@ -1,7 +1,7 @@
 """One attention layer with Q4_K weights, served: two prompts, a few tokens of
 decoding, a beam fork and a compaction of the page pool.
 
-    python examples/attention_layer.py
+    python examples/attention_layer.py [--four-bits]
 
 The layer's projections are the quantized products, its cache the paged one:
 quantize -> qkv product -> rotary positions and append -> attention over the
@@ -31,7 +31,7 @@ class Layer:
     """hidden -> hidden, `heads` query and `kv_heads` key and value heads."""
 
     def __init__(self, hidden=1024, heads=8, kv_heads=2, dim=128, slots=4, pages=64, page=16, width=24, window=0,
-                 sinks=0, seed=1):
+                 sinks=0, seed=1, four_bits=False):
         g = wl.rng(seed)
         self.hidden, self.heads, self.kv_heads, self.dim = hidden, heads, kv_heads, dim
         self.rows, self.page, self.window, self.sinks = (heads + 2 * kv_heads) * dim, page, window, sinks
@@ -42,8 +42,15 @@ class Layer:
         i = torch.arange(dim // 2, dtype=torch.float64, device=DEV)
         self.rope = xq.xq_rope_plan(10000.0 ** (-2.0 * i / dim), [dim // 2])
         shape = (pages, kv_heads, page, dim)
-        self.kv = xq.xq_kv_cache(torch.zeros(shape, dtype=torch.bfloat16, device=DEV),
-                                 torch.zeros(shape, dtype=torch.bfloat16, device=DEV))
+        if four_bits:
+            pools = [torch.zeros(*shape[:3], dim // 2, dtype=torch.uint8, device=DEV).view(torch.float4_e2m1fn_x2)
+                     for _ in range(2)]
+            exps = [torch.zeros(*shape[:3], 4 if dim <= 128 else 8, dtype=torch.uint8, device=DEV)
+                    .view(torch.float8_e8m0fnu) for _ in range(2)]
+            self.kv = xq.xq_kv_cache(*pools, k_exp=exps[0], v_exp=exps[1])
+        else:
+            self.kv = xq.xq_kv_cache(torch.zeros(shape, dtype=torch.bfloat16, device=DEV),
+                                     torch.zeros(shape, dtype=torch.bfloat16, device=DEV))
         ints = dict(dtype=torch.int32, device=DEV)
         self.tables = torch.full((slots, width), -1, **ints)
         self.lens, self.refs = torch.zeros(slots, **ints), torch.zeros(pages, **ints)
@@ -121,7 +128,7 @@ class Layer:
 
 
 def main():
-    layer = Layer()
+    layer = Layer(four_bits="--four-bits" in sys.argv[1:])
     g = torch.Generator(device=DEV).manual_seed(2)
     draw = lambda n: torch.randn(n, layer.hidden, device=DEV, generator=g)
     y, _, _ = layer.prompt(draw(70 + 33), [(0, 70), (1, 33)])

@@ -996,8 +996,9 @@ struct Plan {
 // us, 5.9 TB/s, as 95 of them that share; 256 of 500 to 4000 380 us, 6.1 TB/s)
 // and far from it where one is much longer: 96 sequences, one of 131072 and 95
 // of 1000, take 1.38 ms, with 94 of 1000, shared, 161 us.
-// (A step of 4 bits is 256 tokens, three are 768: 32 sequences of 512 take 12 us
-// unshared, 19 shared; 2048 tokens are faster shared.)
+// (A step of 4 bits is 256 tokens, three are 768: unshared and shared, 1 sequence
+// of 512 8.9 and 12.2 us, of 700 10.5 and 11.6, 16 of 768 11.5 and 14.3, 32 of 768
+// 12.6 and 13.4, bf16 rows.)
 Plan plan(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_len, int64_t window,
           int64_t sinks) {
   Plan p;

@@ -3,6 +3,9 @@ read back, attention element by element with the tolerances of kv_reference (whi
 
 Weights enter their product with v as bf16 pieces: two (2^-16) for a 16-bit output, three (2^-24) for f32's; a chunk's
 as one rounding of its type. q is exact in its pieces. Unused slots, pages and unseen tokens hold NaN (power 255)."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -505,3 +508,43 @@ def test_prompt_then_tokens(io):
         xq.xq_cache_read(back[0], back[1], kv, slots)
         top = x[:, heads + kv_heads:].abs().unflatten(-1, (-1, 32)).amax(-1, keepdim=True).expand(-1, -1, -1, 32).flatten(-2)
         assert ((back[1] - x[:, heads + kv_heads:]).abs() <= top * (2 / 7 + 1e-6)).all()
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
+def test_attention_layer(window, sinks):
+    """The example's layer with its cache in 4 bits: its rows are attention over what the cache holds, through a prompt,
+    single tokens, a fork and a compaction."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_layer.py")
+    spec = importlib.util.spec_from_file_location("attention_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer = example.Layer(window=window, sinks=sinks, four_bits=True)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    draw = lambda n: torch.randn(n, layer.hidden, device=DEV, generator=g)
+
+    def holds(out, q, rows, io):
+        raw = {n: getattr(layer.kv, n).view(torch.uint8) for n in ("k", "v", "k_exp", "v_exp")}
+        s = dict(raw, table=layer.tables, page=layer.page, scale=layer.scale, scales=(1.0, 1.0), q=q)
+        for t, (slot, pos) in enumerate(rows):
+            n = layer.lens.tolist()[slot]
+            want, mag, slack = four.attend(s, slice(t, t + 1), slot, torch.tensor([pos], device=DEV), n, window, sinks)
+            tol = ref.attend_tolerance(want, mag, slack, io, 2.0 ** -8 if io == "bf16" else 2.0 ** -24, n)
+            # A weight is f32, of the largest's 1: below 2^-126 it may count as 0, which takes up to 2^-126 |v| a token from
+            # a sum that is divided by 1 or more. (Scores reach 100 here and many v are 0, so such weights stand alone.)
+            v, _ = four.rows_of(s["v"], s["v_exp"], s["table"][slot], n, s["page"])
+            tol = tol + 2.0 ** -126 * n * v.abs().max()
+            assert ((out[t:t + 1].double() - want).abs() <= tol).all(), (slot, pos)
+
+    last = lambda slots: [(s, layer.lens[s].item() - 1) for s in slots]
+    y, out, q = layer.prompt(draw(103), [(0, 70), (1, 33)])
+    holds(out, q, [(0, p) for p in range(70)] + [(1, p) for p in range(33)], "bf16")
+    y, out, q = layer.step(draw(2), [0, 1])
+    holds(out, q, last([0, 1]), "f32")
+    layer.fork([0, 0], [2, 3])
+    y, out, q = layer.step(draw(4), [0, 1, 2, 3])
+    holds(out, q, last(range(4)), "f32")
+    layer.fork([3], [1])
+    layer.compact()
+    y, out, q = layer.step(draw(4), [0, 1, 2, 3])
+    holds(out, q, last(range(4)), "f32")
+    assert y.isfinite().all()
