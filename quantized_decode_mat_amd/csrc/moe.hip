@@ -9,9 +9,9 @@
 // launches beside them (tens of MB are 6 us). So a token's layer is two launches:
 // gate and up with the product of their results, then down with the sum over the
 // slots. Each workgroup of the first quantizes x for itself, and each of the
-// second the h that it needs, while its first weights are on their way. With
-// more tokens the work is an expert's: the pairs (token, slot) that chose it
-// share one pass over its rows.
+// second the h that it needs, while its first weights are on their way. Where
+// many tokens share experts the work is an expert's: the pairs (token, slot) that
+// chose it share one pass over its rows.
 //
 // A row's dot is the mat-vec's (q4k_row.h): four lanes a super-block. Rows of
 // at most 8 or 4 blocks take a half or a quarter of a wave, which then holds
@@ -258,51 +258,47 @@ __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 // ---- Few pairs an expert: mat-vecs.
 
 // Rows of weights that a wave's lanes have in flight, and rows of h that they make.
-constexpr int up_steps(int nt) { return nt == 1 ? 4 : 2; }
-constexpr int up_rows(int nt, int lpr) { return up_steps(nt) * (kWave / lpr) / 2; }
+constexpr int kUpSteps = 4;
+constexpr int up_rows(int lpr) { return kUpSteps * (kWave / lpr) / 2; }
 
+// Gate and up, and silu(gate) * up, of one pair. LPR: lanes of a row (nb <= LPR / 4
+// where it is below 64). A workgroup has W waves, each `groups` times R rows of h
+// of pair blockIdx.y.
+//
 // What bounds it: the weights' bytes, and with 10 to 25 KB a wave in all the start
 // of that stream (ids, then the first weights; x is quantized meanwhile). Four
-// rows of weights in flight hide it for one pair; two where the pairs of a pass
-// take their registers. Nothing around the loads is conditional, so that the
-// compiler lets them pass the dots before them (five tokens' layer 68 -> 43 us with that, all
-// workgroups on the card at once, and reciprocals in place of divisions).
-// Measured: 8 pairs, 2 x 1536 rows of 2048 columns, 28 MB: 8.0 to 9.7 us; 30 pairs of
-// about 28 experts, 2 x 1280 rows, 73 MB: 25 us.
-//
-// Gate and up, and silu(gate) * up. NT: pairs of one pass. LPR: lanes of a row
-// (nb <= LPR / 4 where it is below 64). A workgroup has W waves, each `groups`
-// times R rows of h, of the expert of pair blockIdx.y.
-template <int NT, int LPR, int W>
+// rows of weights in flight hide it; nothing around the loads is conditional, so
+// that the compiler lets them pass the dots before them. Pairs of one expert are
+// not brought together: they run at the same time, a row's workgroup on the same
+// XCD (the grid's width is a multiple of 8), whose L2 has the second one's reads.
+// (Two pairs a pass, with two rows in flight, were slower but for none: the experts'
+// call with 10 tokens, 6 of 64 experts of 2048 x 1280 67 -> 51 us, 16 tokens, 8 of
+// 128 of 2048 x 768 81 -> 60, 4 tokens, 2 of 8 of 4096 x 14336 160 -> 137; without the
+// multiple of 8 53, 62 and 143.) Measured: 8 pairs, 2 x 1536 rows of 2048 columns, 28
+// MB: 8.0 to 9.7 us.
+template <int LPR, int W>
 __global__ __launch_bounds__(W * kWave, 3) void moe_up_kernel(MoeArgs a) {
   constexpr int SEG = kWave / LPR;            // rows of weights of a wave at a time
-  constexpr int STEPS = up_steps(NT);
-  constexpr int R = up_rows(NT, LPR);
+  constexpr int STEPS = kUpSteps;
+  constexpr int R = up_rows(LPR);
   constexpr int UB = LPR / 4;                 // blocks of a unit
   extern __shared__ __attribute__((aligned(16))) uint8_t act[];
-  __shared__ uint16_t members[NT > 1 ? kMaxPairs : 1];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int pair = blockIdx.y;
-  // One token's x does not wait for the choice of experts. (Two blocks a wave;
-  // 16 blocks, 4096 columns, have more.)
-  constexpr int XE = NT == 1 ? 2 : 1;
+  const int pair = blockIdx.y, from = blockIdx.x * a.groups * W * R;
+  if (from >= a.rows) return;  // (the width's rounding)
+  // x does not wait for the choice of experts. (Two blocks a wave; more than 8
+  // blocks, 2048 columns, take another turn.)
+  constexpr int XE = 2;
+  const uint8_t* x = a.x + div_by(pair, a.used_div) * a.x_row;
   float4 xe[XE];
-  if constexpr (NT == 1) {
 #pragma unroll
-    for (int i = 0; i < XE; ++i) xe[i] = load_x4(a.x, a.x_type, min(wave + i * W, a.nb - 1) * 256 + lane * 4);
-  }
+  for (int i = 0; i < XE; ++i) xe[i] = load_x4(x, a.x_type, min(wave + i * W, a.nb - 1) * 256 + lane * 4);
   const int e = a.ids[pair];
   if (e < 0 || e >= a.experts) return;
-  int count = 1;
-  if constexpr (NT > 1) {
-    count = pairs_of(a.ids, a.tokens * a.used, pair, e, members);
-    if (count == 0) return;  // workgroup-uniform
-  }
-  auto member = [&](int m) { return NT > 1 ? static_cast<int>(members[m]) : pair; };
 
   const LaneGeom L = lane_geom(lane);
   const int seg = lane / LPR, bsub = lane % LPR / 4;
-  const int first = (blockIdx.x * a.groups * W + wave) * R;  // group g's rows begin at first + g * W * R
+  const int first = from + wave * R;          // group g's rows begin at first + g * W * R
   const int64_t row_bytes = static_cast<int64_t>(a.nb) * kQ4KBytes;
   const int units = LPR < kWave ? 1 : (a.nb + UB - 1) / UB;
   auto load = [&](int g, int u, Nib(&n)[STEPS], uint4(&h)[STEPS]) {
@@ -316,90 +312,66 @@ __global__ __launch_bounds__(W * kWave, 3) void moe_up_kernel(MoeArgs a) {
       h[s] = *reinterpret_cast<const uint4*>(blk);
     }
   };
-  const int x_bytes = a.nb * kQ8KBytes;
-  for (int m = 0; m < count; m += NT) {
-    const int here = min(NT, count - m);
-    Nib n0[STEPS], n1[STEPS];
-    uint4 h0[STEPS], h1[STEPS];
-    load(0, 0, n0, h0);
-    if (NT > 1) __syncthreads();  // the members are listed; the pass before is done with the activations
-    if constexpr (NT == 1) {
+  Nib n0[STEPS], n1[STEPS];
+  uint4 h0[STEPS], h1[STEPS];
+  load(0, 0, n0, h0);
 #pragma unroll
-      for (int i = 0; i < XE; ++i)
-        if (wave + i * W < a.nb) q8k_block_wave<true>(xe[i], act + (wave + i * W) * kQ8KBytes, lane);
-    }
-    for (int i = wave + (NT == 1 ? XE * W : 0); i < here * a.nb; i += W) {
-      const int t = NT > 1 ? div_by(i, a.nb_div) : 0, b = i - t * a.nb;
-      const uint8_t* row = a.x + div_by(member(m + t), a.used_div) * a.x_row;
-      q8k_block_wave<true>(load_x4(row, a.x_type, b * 256 + lane * 4), act + i * kQ8KBytes, lane);
-    }
-    __syncthreads();
+  for (int i = 0; i < XE; ++i)
+    if (wave + i * W < a.nb) q8k_block_wave<true>(xe[i], act + (wave + i * W) * kQ8KBytes, lane);
+  for (int i = wave + XE * W; i < a.nb; i += W)
+    q8k_block_wave<true>(load_x4(x, a.x_type, i * 256 + lane * 4), act + i * kQ8KBytes, lane);
+  __syncthreads();
 
-    float acc[STEPS][NT] = {};
-    auto add = [&](int u, const Nib(&n)[STEPS], const uint4(&h)[STEPS]) {
-      const int bb = u * UB + bsub, b = min(bb, a.nb - 1);
-      ChunkDecode c[STEPS];
+  float acc[STEPS] = {};
+  auto add = [&](int u, const Nib(&n)[STEPS], const uint4(&h)[STEPS]) {
+    const int bb = u * UB + bsub, b = min(bb, a.nb - 1);
+    const TokenSlice t = token_slice(act, b, L);
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) c[s] = chunk_decode(n[s], h[s], L);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (NT > 1 && t >= here) break;  // workgroup-uniform
-        const TokenSlice x = token_slice(act + t * x_bytes, b, L);
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          const float v = chunk_token_slice(c[s], x);
-          acc[s][t] += bb < a.nb ? v : 0.f;
-        }
-      }
-    };
-    // A row's sum in the mat-vec's order, each to the lane that stores it: lane
-    // r * NT + t.
-    auto finish = [&](int g) {
-      float mine = 0.f, up = 0.f;
-      static_assert(R * NT <= kWave);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (NT > 1 && t >= here) break;
-        float sums[STEPS * SEG];
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          const float v = row16_sum(acc[s][t]);
-          acc[s][t] = 0.f;
-          if constexpr (LPR == 64) {
-            sums[s] = (readlane(v, 0) + readlane(v, 16)) + (readlane(v, 32) + readlane(v, 48));
-          } else if constexpr (LPR == 32) {
-            sums[s * 2] = readlane(v, 0) + readlane(v, 16);
-            sums[s * 2 + 1] = readlane(v, 32) + readlane(v, 48);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sums[s * 4 + i] = readlane(v, 16 * i);
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          mine = lane == r * NT + t ? sums[2 * r] : mine;
-          up = lane == r * NT + t ? sums[2 * r + 1] : up;
-        }
-      }
-      mine = silu(mine) * up;
-      const int r = lane / NT, t = lane % NT, row = first + g * W * R + r;
-      if (r < R && t < here && row < a.rows) a.out[static_cast<int64_t>(member(m + t)) * a.rows + row] = mine;
-    };
-    // Groups of rows, and units of a row, one after the other; the next one's
-    // weights are on their way while one is worked on.
-    int g = 0, u = 0;
-    auto step = [&](Nib(&n)[STEPS], uint4(&h)[STEPS], Nib(&nn)[STEPS], uint4(&hh)[STEPS]) {
-      const int g1 = u + 1 < units ? g : g + 1, u1 = u + 1 < units ? u + 1 : 0;
-      const bool more = g1 < a.groups && first + g1 * W * R < a.rows;  // wave-uniform
-      if (more) load(g1, u1, nn, hh);
-      add(u, n, h);
-      if (u + 1 == units) finish(g);
-      g = g1;
-      u = u1;
-      return more;
-    };
-    while (step(n0, h0, n1, h1) && step(n1, h1, n0, h0)) {
+    for (int s = 0; s < STEPS; ++s) {
+      const float v = chunk_token_slice(chunk_decode(n[s], h[s], L), t);
+      acc[s] += bb < a.nb ? v : 0.f;
     }
+  };
+  // A row's sum in the mat-vec's order, each to the lane that stores it.
+  auto finish = [&](int g) {
+    float mine = 0.f, up = 0.f, sums[STEPS * SEG];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const float v = row16_sum(acc[s]);
+      acc[s] = 0.f;
+      if constexpr (LPR == 64) {
+        sums[s] = (readlane(v, 0) + readlane(v, 16)) + (readlane(v, 32) + readlane(v, 48));
+      } else if constexpr (LPR == 32) {
+        sums[s * 2] = readlane(v, 0) + readlane(v, 16);
+        sums[s * 2 + 1] = readlane(v, 32) + readlane(v, 48);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[s * 4 + i] = readlane(v, 16 * i);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mine = lane == r ? sums[2 * r] : mine;
+      up = lane == r ? sums[2 * r + 1] : up;
+    }
+    mine = silu(mine) * up;
+    const int row = first + g * W * R + lane;
+    if (lane < R && row < a.rows) a.out[static_cast<int64_t>(pair) * a.rows + row] = mine;
+  };
+  // Groups of rows, and units of a row, one after the other; the next one's
+  // weights are on their way while one is worked on.
+  int g = 0, u = 0;
+  auto step = [&](Nib(&n)[STEPS], uint4(&h)[STEPS], Nib(&nn)[STEPS], uint4(&hh)[STEPS]) {
+    const int g1 = u + 1 < units ? g : g + 1, u1 = u + 1 < units ? u + 1 : 0;
+    const bool more = g1 < a.groups && first + g1 * W * R < a.rows;  // wave-uniform
+    if (more) load(g1, u1, nn, hh);
+    add(u, n, h);
+    if (u + 1 == units) finish(g);
+    g = g1;
+    u = u1;
+    return more;
+  };
+  while (step(n0, h0, n1, h1) && step(n1, h1, n0, h0)) {
   }
 }
 
@@ -739,36 +711,23 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
   store_from_f32(a.y + token * a.y_row, a.type, row, sum);
 }
 
-// The same bound from every call, so that calls of several threads do not lower
-// one another's.
-constexpr int kMostLds = 80 * 1024;
-template <class Kernel>
-hipError_t allow_lds(Kernel kernel, size_t lds) {
-  if (lds <= 48 * 1024) return hipSuccess;
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
-}
-
-template <int NT, int LPR>
+template <int LPR>
 hipError_t launch_up(MoeArgs a, hipStream_t stream) {
-  constexpr int W = 4, R = up_rows(NT, LPR);
-  const size_t lds = static_cast<size_t>(NT) * a.nb * kQ8KBytes;  // (2 x 128 blocks at most)
-  auto kernel = moe_up_kernel<NT, LPR, W>;
-  if (const hipError_t e = allow_lds(kernel, lds); e != hipSuccess) return e;
+  constexpr int W = 4, R = up_rows(LPR);
+  const size_t lds = static_cast<size_t>(a.nb) * kQ8KBytes;  // (of 128 blocks at most, 40 KiB)
   const int64_t pairs = static_cast<int64_t>(a.tokens) * a.used;
   // So many groups a wave that all workgroups are on the card at once.
-  constexpr int64_t kRoom = 256 * 3;
-  const int64_t tiles = (a.rows + W * R - 1) / (W * R);
-  a.groups = static_cast<int>((tiles * pairs + kRoom - 1) / kRoom);
-  const int64_t blocks = (tiles + a.groups - 1) / a.groups;
-  kernel<<<dim3(static_cast<uint32_t>(blocks), static_cast<uint32_t>(pairs)), dim3(W * kWave), lds, stream>>>(a);
+  const int64_t room = std::max<int64_t>(8, 256 * 3 / pairs / 8 * 8), tiles = (a.rows + W * R - 1) / (W * R);
+  a.groups = static_cast<int>((tiles + room - 1) / room);
+  const int64_t blocks = ((tiles + a.groups - 1) / a.groups + 7) / 8 * 8;
+  moe_up_kernel<LPR, W><<<dim3(static_cast<uint32_t>(blocks), static_cast<uint32_t>(pairs)), dim3(W * kWave), lds, stream>>>(a);
   return hipGetLastError();
 }
 
-template <int NT>
-hipError_t launch_lanes(const MoeArgs& a, hipStream_t stream) {
-  if (a.nb <= 4) return launch_up<NT, 16>(a, stream);
-  if (a.nb <= 8) return launch_up<NT, 32>(a, stream);
-  return launch_up<NT, 64>(a, stream);
+hipError_t launch_up_of(const MoeArgs& a, hipStream_t stream) {
+  if (a.nb <= 4) return launch_up<16>(a, stream);
+  if (a.nb <= 8) return launch_up<32>(a, stream);
+  return launch_up<64>(a, stream);
 }
 
 template <int MATS>
@@ -788,11 +747,18 @@ hipError_t launch_pack(uint8_t* packed, float* scales, const uint8_t* x, int64_t
 }
 
 constexpr int kDownWaves = 8;
+constexpr int kMostDownLds = 80 * 1024;  // two workgroups a CU
 template <int PF>
 hipError_t launch_down(MoeArgs a, hipStream_t stream) {
   const size_t lds = static_cast<size_t>(a.used) * a.nb * kQ8KBytes;
   auto kernel = moe_down_kernel<kDownWaves, PF>;
-  if (const hipError_t e = allow_lds(kernel, lds); e != hipSuccess) return e;
+  // (The same bound from every call, so that calls of several threads do not
+  // lower one another's.)
+  if (lds > 48 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kMostDownLds);
+    if (e != hipSuccess) return e;
+  }
   // So many rows a wave that all workgroups are on the card at once, one a CU.
   const int per_token = std::max(1, 256 / a.tokens);
   a.groups = (a.rows + per_token * kDownWaves - 1) / (per_token * kDownWaves);
@@ -801,17 +767,21 @@ hipError_t launch_down(MoeArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Mat-vecs, and down token by token, where tokens hardly share experts (as many
-// experts as pairs and more) and a token's h fits a workgroup's LDS (two
-// workgroups a CU). The experts' call alone, mat-vecs against tiles, us:
-//   8 experts, 4096 x 14336, 2 used: 1 token 55 / 86, 2 87 / 102, 3 123 / 133,
-//     4 160 / 142, 8 325 / 185
-//   64 experts, 2048 x 1536, 8 used: 1 token 16 / 29, 2 24 / 39
-//   64 experts, 2048 x 1280, 6 used: 5 tokens 32 / 55, 10 67 / 74, 16 91 / 91
-//   128 experts, 2048 x 768, 8 used: 16 tokens 81 / 90
-//   16 experts, 1024 x 1024, 4 used: 4 tokens 14 / 22, 8 20 / 26
-bool by_rows(int64_t tokens, int64_t used, int64_t experts, int64_t ffn) {
-  return (tokens == 1 || tokens * used <= experts) && used * (ffn / 256) * kQ8KBytes <= kMostLds;
+// Mat-vecs, pair by pair and token by token, where they read hardly more than each
+// expert once, or where what they read again (from the caches) is less than the
+// tiles' launches and passes cost; and a token's h has to fit a workgroup's LDS.
+// The experts' call alone, mat-vecs against tiles, us, by tokens:
+//   8 experts of 4096 x 14336, 2 used: 2 87 / 109, 4 138 / 147, 5 172 / 153, 8 246 / 182
+//   64 experts of 2048 x 1280, 6 used: 8 41 / 67, 16 69 / 90, 24 104 / 104, 48 163 / 122
+//   128 experts of 2048 x 768, 8 used: 16 60 / 90, 32 103 / 126, 64 170 / 165
+//   8 experts of 2048 x 4096, 2 used: 4 23 / 40, 8 33 / 47, 16 52 / 49, 32 90 / 50
+//   16 experts of 1024 x 1024, 4 used: 4 13 / 22, 16 21 / 28, 32 31 / 29
+// (The rule turns to tiles at 5, 25, 45, 11 and 34 tokens. An expert costs the tiles a
+// start and a tile that is not full, beside what every call costs.)
+bool by_rows(int64_t tokens, int64_t used, int64_t experts, int64_t hidden, int64_t ffn) {
+  const int64_t pairs = tokens * used, bytes = 3 * (hidden / 256) * ffn * kQ4KBytes;
+  return (pairs <= experts || (pairs - experts) * bytes <= 150000000 + experts * 3500000) &&
+         used * (ffn / 256) * kQ8KBytes <= kMostDownLds;
 }
 
 struct Layout {
@@ -914,8 +884,8 @@ hipError_t launch_moe_q4k(void* y, int64_t y_row, const void* x, int64_t x_row, 
   d.nb_div = fast_div(static_cast<uint32_t>(d.nb));
   d.x = w + l.h;
   hipError_t e;
-  if (by_rows(tokens, used, experts, ffn)) {
-    if ((e = tokens == 1 ? launch_lanes<1>(a, stream) : launch_lanes<2>(a, stream)) != hipSuccess) return e;
+  if (by_rows(tokens, used, experts, hidden, ffn)) {
+    if ((e = launch_up_of(a, stream)) != hipSuccess) return e;
     const int64_t steps = (used * d.nb + kUnitBlocks - 1) / kUnitBlocks;
     if (steps == 1) return launch_down<1>(d, stream);
     if (steps == 2) return launch_down<2>(d, stream);

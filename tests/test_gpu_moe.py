@@ -131,11 +131,11 @@ LAYERS = [
     (1, 8, 16, 256, 11264, "bf16"),     # h past 80 KiB of LDS: by tiles
     (2, 3, 60, 768, 512, "f32"),
     (5, 6, 64, 2048, 1280, "f16"),
-    (7, 1, 8, 8448, 512, "bf16"),       # three units, two pairs a pass
+    (7, 1, 8, 8448, 512, "bf16"),       # three units
     (3, 2, 8, 1024, 1792, "f32"),
     (9, 4, 8, 512, 768, "bf16"),
-    (16, 2, 8, 1024, 1280, "f32"),      # tiles
-    (40, 2, 2, 512, 256, "f16"),        # 40 pairs an expert: three passes
+    (16, 2, 8, 1024, 1280, "f32"),
+    (40, 2, 2, 512, 256, "f16"),
     (33, 3, 5, 256, 2304, "bf16"),
     (512, 1, 3, 256, 256, "f32"),
     (16, 8, 128, 768, 256, "bf16"),
@@ -146,6 +146,14 @@ LAYERS = [
     (3, 1, 2, 256, 32768, "f32"),
     (5, 1, 2, 32768, 512, "bf16"),
     (1, 512, 1024, 256, 256, "f32"),    # all 512 slots a token's
+    (16, 2, 8, 2304, 2048, "f32"),      # many pairs of larger experts: tiles
+    (40, 2, 2, 2048, 2304, "f16"),      # 40 pairs an expert: three passes
+    (33, 3, 5, 1024, 2304, "bf16"),
+    (9, 4, 8, 2048, 2816, "bf16"),
+    (512, 1, 3, 2048, 1024, "f32"),
+    (64, 8, 64, 1024, 1024, "f16"),
+    (512, 1, 1, 768, 512, "bf16"),
+    (17, 1, 2, 32768, 256, "f32"),
 ]
 
 
@@ -164,9 +172,9 @@ def test_layer(case):
     assert not s["ws"][:96 * 1024].any(), "wrote where other calls keep counters"
 
 
-@pytest.mark.parametrize("tokens,experts", [(1, 16), (3, 16), (12, 6)])
-def test_slots_left_out_and_experts_named_twice(tokens, experts):
-    c = dict(tokens=tokens, used=4, experts=experts, hidden=512, ffn=512, io="f32")
+@pytest.mark.parametrize("tokens,experts,width", [(1, 16, 512), (3, 16, 512), (12, 6, 512), (100, 6, 1024)])  # the last by tiles
+def test_slots_left_out_and_experts_named_twice(tokens, experts, width):
+    c = dict(tokens=tokens, used=4, experts=experts, hidden=width, ffn=width, io="f32")
     s = state(c, 2)
     s["ids"][0] = torch.tensor([-1, 3, 3, experts], dtype=torch.int32)
     if tokens > 1:
@@ -181,10 +189,10 @@ def test_slots_left_out_and_experts_named_twice(tokens, experts):
     check(c, s)
 
 
-@pytest.mark.parametrize("tokens", [1, 6])
-def test_rows_of_zeros_and_large_weights(tokens):
+@pytest.mark.parametrize("tokens,experts", [(1, 2), (6, 12), (96, 4)])  # the last by tiles
+def test_rows_of_zeros_and_large_weights(tokens, experts):
     """x of zeros gives zeros; q8_K blocks of zeros beside others; weights at the header's ends."""
-    c = dict(tokens=tokens, used=2, experts=2 * tokens, hidden=1024, ffn=768, io="f32")
+    c = dict(tokens=tokens, used=2, experts=experts, hidden=1024, ffn=768, io="f32")
     s = state(c, 3)
     s["x"][0] = 0
     if tokens > 1:
@@ -202,8 +210,8 @@ def test_rows_of_zeros_and_large_weights(tokens):
 
 
 def test_layer_in_a_graph_on_another_stream():
-    for tokens in (1, 4, 20):
-        c = dict(tokens=tokens, used=3, experts=12, hidden=512, ffn=768, io="bf16")
+    for tokens, hidden, ffn in ((1, 512, 768), (4, 512, 768), (20, 512, 768), (40, 1024, 2048)):  # the last by tiles
+        c = dict(tokens=tokens, used=3, experts=12, hidden=hidden, ffn=ffn, io="bf16")
         s = state(c, 4)
         run(c, s)
         torch.cuda.synchronize()
@@ -214,7 +222,7 @@ def test_layer_in_a_graph_on_another_stream():
         with torch.cuda.graph(graph, stream=side):
             run(c, s)
         for _ in range(3):
-            s["full"][:, :512] = 5.0
+            s["full"][:, :hidden] = 5.0
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(s["y"], want)
@@ -227,7 +235,7 @@ def test_two_layers_at_once():
     """Two streams, each with its own workspace, and x of one in both."""
     g = torch.Generator(device=DEV).manual_seed(6)
     runs = []
-    for tokens, experts in ((1, 8), (3, 40), (24, 8)):
+    for tokens, experts in ((1, 8), (3, 40), (48, 8)):  # the last by tiles
         c = dict(tokens=tokens, used=4, experts=experts, hidden=1024, ffn=768, io="bf16")
         a = state(c, 7)
         b = dict(a, ids=torch.randint(0, experts, (tokens, 4), device=DEV, generator=g, dtype=torch.int32),
