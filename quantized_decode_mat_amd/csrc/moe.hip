@@ -716,10 +716,19 @@ hipError_t launch_up(MoeArgs a, hipStream_t stream) {
   constexpr int W = 4, R = up_rows(LPR);
   const size_t lds = static_cast<size_t>(a.nb) * kQ8KBytes;  // (of 128 blocks at most, 40 KiB)
   const int64_t pairs = static_cast<int64_t>(a.tokens) * a.used;
-  // So many groups a wave that all workgroups are on the card at once.
-  const int64_t room = std::max<int64_t>(8, 256 * 3 / pairs / 8 * 8), tiles = (a.rows + W * R - 1) / (W * R);
-  a.groups = static_cast<int>((tiles + room - 1) / room);
-  const int64_t blocks = ((tiles + a.groups - 1) / a.groups + 7) / 8 * 8;
+  // So many groups a wave that all workgroups are on the card at once, three a CU,
+  // or two where the busiest CU has less to do then: five tokens, 6 of 64 experts
+  // of 2048 x 1280, are 600 workgroups of 4 groups or 480 of 5, 33.5 and 30.3 us.
+  const int64_t tiles = (a.rows + W * R - 1) / (W * R);
+  int64_t blocks = 0, least = 0;
+  for (int64_t per_cu = 3; per_cu >= 2; --per_cu) {
+    const int64_t room = std::max<int64_t>(8, 256 * per_cu / pairs / 8 * 8), groups = (tiles + room - 1) / room;
+    const int64_t used = (tiles + groups - 1) / groups, busiest = groups * ((used * pairs + 255) / 256);
+    if (blocks && busiest >= least) continue;
+    least = busiest;
+    a.groups = static_cast<int>(groups);
+    blocks = (used + 7) / 8 * 8;
+  }
   moe_up_kernel<LPR, W><<<dim3(static_cast<uint32_t>(blocks), static_cast<uint32_t>(pairs)), dim3(W * kWave), lds, stream>>>(a);
   return hipGetLastError();
 }
