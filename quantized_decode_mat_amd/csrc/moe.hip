@@ -18,8 +18,9 @@
 // two or four rows, gate's and up's next to each other.
 //
 // Measured, router and experts together: one token, 8 of 64 experts, 2048 x 1536:
-// 21.6 us (43 MB; 5.9 at a streaming read's rate); five tokens, 6 of 64, 2048 x
-// 1280: 42.8 (110 MB, 15); 16 tokens, 2 of 8, 4096 x 14336: 205 us (785 MB, 108).
+// 21.8 us (43 MB; 5.9 at a streaming read's rate); five tokens, 6 of 64, 2048 x
+// 1280: 38.8 (110 MB, 15); 16 tokens, 2 of 8, 4096 x 14336: 202 to 217 us by card
+// (785 MB, 108).
 //
 // Precision: the products are whole numbers up to the scales, sums over blocks
 // and slots f32. The activations go to q8_K twice, as the mat-vecs' do; h stays
@@ -275,7 +276,7 @@ constexpr int up_rows(int lpr) { return kUpSteps * (kWave / lpr) / 2; }
 // call with 10 tokens, 6 of 64 experts of 2048 x 1280 67 -> 51 us, 16 tokens, 8 of
 // 128 of 2048 x 768 81 -> 60, 4 tokens, 2 of 8 of 4096 x 14336 160 -> 137; without the
 // multiple of 8 53, 62 and 143.) Measured: 8 pairs, 2 x 1536 rows of 2048 columns, 28
-// MB: 8.0 to 9.7 us.
+// MB: 8.0 to 9.9 us; 30 pairs, 2 x 1280 rows, 73 MB: 17.6, 4.2 TB/s.
 template <int LPR, int W>
 __global__ __launch_bounds__(W * kWave, 3) void moe_up_kernel(MoeArgs a) {
   constexpr int SEG = kWave / LPR;            // rows of weights of a wave at a time
