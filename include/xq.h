@@ -636,7 +636,7 @@ size_t xq_moe_route_workspace_bytes(int64_t tokens, int64_t experts);  /* 0 if t
  * x is to be finite, as for xq_quantize_q8k.
  *  y, x    device [tokens][hidden] of type io (XQ_F32, XQ_BF16, XQ_F16), rows
  *          y_row and x_row elements apart; x and its rows 16-byte aligned, y
- *          aligned to its elements.
+ *          aligned to its elements. y may be x where the strides are the same.
  *  gate, up  device Q4_K, `experts` experts of ffn rows of hidden columns back to
  *          back; down the same of hidden rows of ffn columns. 16-byte aligned.
  *  ids     device int32[tokens][used], weights device f32[tokens][used].

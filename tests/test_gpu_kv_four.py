@@ -85,6 +85,9 @@ APPEND = [
     (65, 16, 2, 256, 256, [128], False, 64, "f16", "f16", "nhd"),
     (2100, 3, 1, 224, 8, [4], False, 32, "f32", "bf16", "hnd"),
     (300, 1, 1, 192, 192, [96], True, 16, "bf16", "bf16", "hnd"),
+    (4097, 4, 2, 128, 128, [24, 20, 20], False, 16, "bf16", "bf16", "nhd"),  # four tokens a workgroup
+    (5002, 1, 1, 32, 16, [8], True, 64, "f32", "f16", "hnd"),
+    (4099, 3, 9, 256, 200, [60, 40], False, 8, "f16", "f32", "hnd"),         # more than 256 quarters a token
 ]
 
 
@@ -176,6 +179,19 @@ def test_append_borders_zeros_and_what_is_not_finite():
         assert back[0, 26, 0, :32].isnan().all() and back[1, 26, 0, 32:64].isnan().all()
         assert back[0, 25, 0, :32].isnan().all()            # an infinity turned: 0 times it is NaN
         assert int(back.isnan().sum()) == 96
+
+
+@pytest.mark.parametrize("rot,src", [(128, "bf16"), (40, "f32"), (72, "f16")])
+def test_append_with_q_in_place(rot, src):
+    """q_out is q, among k and v in one product's output."""
+    s = append_state((70, 6, 2, 128, rot, [rot // 2], False, 16, src, src, "hnd"))
+    before = {n: s[n].clone() for n in ("k", "v", "k_exp", "v_exp")}
+    x = s["x"].clone()
+    s["out"] = s["x"]
+    append(s, 6, 2, (0.75, 1.25))
+    check_rope(s["x"][:, :6], x[:, :6], s["pos"], s["plan"], [rot // 2], False, False, src)
+    assert torch.equal(s["x"][:, 6:], x[:, 6:])
+    check_append(dict(s, x=x), before, 6, 2, [rot // 2], False, (0.75, 1.25))
 
 
 def test_append_of_unaligned_rows():

@@ -231,6 +231,19 @@ def test_layer_in_a_graph_on_another_stream():
             assert torch.equal(s["y"], want)
 
 
+@pytest.mark.parametrize("tokens,hidden,ffn", [(1, 512, 768), (5, 512, 768), (60, 1024, 2048)])  # the last by tiles
+def test_layer_in_place(tokens, hidden, ffn):
+    c = dict(tokens=tokens, used=3, experts=6, hidden=hidden, ffn=ffn, io="bf16")
+    s = state(c, 11)
+    run(c, s)
+    torch.cuda.synchronize()
+    want = s["y"].clone()
+    s["y"] = s["x"]
+    run(c, s)
+    torch.cuda.synchronize()
+    assert torch.equal(s["x"], want)
+
+
 def test_two_layers_at_once():
     """Two streams, each with its own workspace, and x of one in both."""
     g = torch.Generator(device=DEV).manual_seed(6)
