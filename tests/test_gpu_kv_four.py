@@ -372,6 +372,44 @@ def test_decode_in_a_graph_on_another_stream():
         assert torch.equal(s["out"], want)
 
 
+def test_decode_at_once_on_two_streams():
+    """A call whose parts are joined, one whose are not, and one of many parts, each on two streams."""
+    runs = []
+    for lens, heads, io in (([5000, 300], 8, "f32"), ([700, 40], 8, "bf16"), ([9000], 4, "f16")):
+        a, b = (setup(lens, heads, 2, 128, 16, io, "hnd", seed=seed) for seed in (1, 2))
+        runs.append((lens, a, b, decode(a, 0, 0, max(lens)), decode(b, 0, 0, max(lens))))
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for lens, a, b, wa, wb in runs:
+        a["full"][:, :a["q"].shape[1]] = 5.0
+        b["full"][:, :b["q"].shape[1]] = 5.0
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for lens, a, b, wa, wb in runs:
+            decode(a, 0, 0, max(lens), wa, stream=one)
+            decode(b, 0, 0, max(lens), wb, stream=two)
+    for lens, a, b, wa, wb in runs:
+        check_single(a, lens, 0, 0, "first stream")
+        check_single(b, lens, 0, 0, "second stream")
+
+
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 1e-30, -1e-40])
+def test_scales_of_scores(scale):
+    """Negative: the order of the scores turns round; 0: all tokens weigh the same."""
+    lens = [1900, 33, 0, 600]
+    s = setup(lens, 8, 2, 128, 16, "f32", "nhd")
+    s["scale"] = scale
+    decode(s, 0, 0, 1900)
+    check_single(s, lens, 0, 0, "scale %g" % scale)
+    decode(s, 100, 3, 1900)
+    check_single(s, lens, 100, 3, "scale %g, window" % scale)
+    for lens, chunks, heads in (([300, 90], [200, 60], 4), ([900, 1000], [900, 1000], 16)):
+        s = setup(lens, heads, 4, 64, 16, "bf16", "hnd", rows=sum(chunks))
+        s["scale"] = scale
+        starts = prefill(s, chunks, 70, 3)
+        check_chunks(s, lens, chunks, starts, 70, 3, "chunk, scale %g" % scale)
+
+
 CHUNK = [
     # lens, chunks, heads, kv_heads, dim, page, io, order, window, sinks, copies
     ([70, 5, 300], [70, 1, 33], 8, 2, 128, 16, "bf16", "hnd", 0, 0),
