@@ -881,82 +881,82 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       // eight parts are read as agent-scope atomics of 8 bytes instead: 32
       // sequences of 2048 27.3 -> 23.7 us. With 32 parts those lose, 18.4 -> 20.6.)
       auto join = [&](auto atomics) {
-      constexpr bool kAtomics = decltype(atomics)::value;
-      if constexpr (!kAtomics) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-      auto one = [&](const float* p) {
-        if constexpr (kAtomics) return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        else return *p;
-      };
-      auto four = [&](const float* p) {
-        if constexpr (!kAtomics) return *reinterpret_cast<const f32x4*>(p);
-        const uint64_t* w = reinterpret_cast<const uint64_t*>(p);
-        const uint64_t lo = __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const uint64_t hi = __hip_atomic_load(w + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        return __builtin_bit_cast(f32x4, u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
-                                               static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)});
-      };
-      const float* p_first = a.part + (2 * g0 + second) * part_size;
-      const float* p_rest = a.part + 2 * g0 * part_size;  // part i > 0 is p_step * i on
-      const int64_t p_step = 2 * per_seq * part_size;
-      auto part = [&](int i) { return i ? p_rest + i * p_step : p_first; };
-      // A thread adds up four outputs over every `teams`th part, then the teams
-      // are added up. The first of its loads go out ahead of those that the
-      // factors wait for.
-      constexpr int kAhead = 8;
-      const int quads = heads * DP / 4, teams = join_teams(kThreads, quads);
-      const int team = tid % teams;
-      f32x4 ahead[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        ahead[k] = four(part(min(team + k * teams, parts - 1)) + min(tid / teams, quads - 1) * 4);
-      // The parts' factors exp(m - max m) / sum, [head][part], in LDS.
-      for (int r = wave; r < heads; r += kWaves) {
-        const float* ml = part(min(lane, parts - 1)) + heads * DP + r;
-        const float m0 = lane < parts ? one(ml) : -INFINITY, l0 = one(ml + heads);
-        float top = m0;
-        for (int i = lane + kWave; i < parts; i += kWave) top = fmaxf(top, one(part(i) + heads * DP + r));
-        top = wave_max(top);
-        const float base = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        for (int i = lane; i < parts; i += kWave) {
-          const float* p = part(i) + heads * DP + r;
-          const float f = exp2_fast((i < kWave ? m0 : one(p)) - base);
-          lds[r * parts + i] = f;
-          sum += f * (i < kWave ? l0 : one(p + heads));
-        }
-        sum = wave_sum(sum);
-        const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
-        for (int i = lane; i < parts; i += kWave) lds[r * parts + i] *= inv;
-      }
-      __syncthreads();
-      f32x4* sums = reinterpret_cast<f32x4*>(lds + (heads * parts + 3) / 4 * 4);
-      for (int q0 = 0; q0 < quads; q0 += kThreads / teams) {
-        const int q = q0 + tid / teams, r = q * 4 / DP, d = q * 4 % DP;
-        f32x4 x = zero4;
-        if (q < quads) {
-          int i = team;
-          if (q0 == 0) {
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k, i += teams)
-              if (i < parts) x += lds[r * parts + i] * ahead[k];
+        constexpr bool kAtomics = decltype(atomics)::value;
+        if constexpr (!kAtomics) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        auto one = [&](const float* p) {
+          if constexpr (kAtomics) return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          else return *p;
+        };
+        auto four = [&](const float* p) {
+          if constexpr (!kAtomics) return *reinterpret_cast<const f32x4*>(p);
+          const uint64_t* w = reinterpret_cast<const uint64_t*>(p);
+          const uint64_t lo = __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          const uint64_t hi = __hip_atomic_load(w + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          return __builtin_bit_cast(f32x4, u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                                                 static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)});
+        };
+        const float* p_first = a.part + (2 * g0 + second) * part_size;
+        const float* p_rest = a.part + 2 * g0 * part_size;  // part i > 0 is p_step * i on
+        const int64_t p_step = 2 * per_seq * part_size;
+        auto part = [&](int i) { return i ? p_rest + i * p_step : p_first; };
+        // A thread adds up four outputs over every `teams`th part, then the teams
+        // are added up. The first of its loads go out ahead of those that the
+        // factors wait for.
+        constexpr int kAhead = 8;
+        const int quads = heads * DP / 4, teams = join_teams(kThreads, quads);
+        const int team = tid % teams;
+        f32x4 ahead[kAhead];
+  #pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          ahead[k] = four(part(min(team + k * teams, parts - 1)) + min(tid / teams, quads - 1) * 4);
+        // The parts' factors exp(m - max m) / sum, [head][part], in LDS.
+        for (int r = wave; r < heads; r += kWaves) {
+          const float* ml = part(min(lane, parts - 1)) + heads * DP + r;
+          const float m0 = lane < parts ? one(ml) : -INFINITY, l0 = one(ml + heads);
+          float top = m0;
+          for (int i = lane + kWave; i < parts; i += kWave) top = fmaxf(top, one(part(i) + heads * DP + r));
+          top = wave_max(top);
+          const float base = top == -INFINITY ? 0.f : top;
+          float sum = 0.f;
+          for (int i = lane; i < parts; i += kWave) {
+            const float* p = part(i) + heads * DP + r;
+            const float f = exp2_fast((i < kWave ? m0 : one(p)) - base);
+            lds[r * parts + i] = f;
+            sum += f * (i < kWave ? l0 : one(p + heads));
           }
-#pragma unroll 8
-          for (; i < parts; i += teams)
-            x += lds[r * parts + i] * four(part(i) + q * 4);
+          sum = wave_sum(sum);
+          const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+          for (int i = lane; i < parts; i += kWave) lds[r * parts + i] *= inv;
         }
-        if (teams > 1) {
-          sums[tid] = x;
-          __syncthreads();
-          if (join_adds(tid, teams, quads - q0))
-            for (int i = 1; i < teams; ++i) x += sums[tid + i];
-          __syncthreads();
+        __syncthreads();
+        f32x4* sums = reinterpret_cast<f32x4*>(lds + (heads * parts + 3) / 4 * 4);
+        for (int q0 = 0; q0 < quads; q0 += kThreads / teams) {
+          const int q = q0 + tid / teams, r = q * 4 / DP, d = q * 4 % DP;
+          f32x4 x = zero4;
+          if (q < quads) {
+            int i = team;
+            if (q0 == 0) {
+  #pragma unroll
+              for (int k = 0; k < kAhead; ++k, i += teams)
+                if (i < parts) x += lds[r * parts + i] * ahead[k];
+            }
+  #pragma unroll 8
+            for (; i < parts; i += teams)
+              x += lds[r * parts + i] * four(part(i) + q * 4);
+          }
+          if (teams > 1) {
+            sums[tid] = x;
+            __syncthreads();
+            if (join_adds(tid, teams, quads - q0))
+              for (int i = 1; i < teams; ++i) x += sums[tid + i];
+            __syncthreads();
+          }
+          if (join_adds(tid, teams, quads - q0) && d < a.dim) {
+  #pragma unroll
+            for (int i = 0; i < 4; ++i)
+              store_from_f32(a.out + row_at(r, a.out_row, a.out_head), IO, d + i, x[i]);
+          }
         }
-        if (join_adds(tid, teams, quads - q0) && d < a.dim) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            store_from_f32(a.out + row_at(r, a.out_row, a.out_head), IO, d + i, x[i]);
-        }
-      }
       };
       if constexpr (F4) {
         if (parts <= 8) join(std::true_type{});

@@ -335,8 +335,9 @@ __device__ __forceinline__ void store8(uint8_t* p, int type, int at, const float
 }
 
 // The append to a cache of 4 bits. The first workgroups turn q, as rope_kernel
-// does (WIDE: 16 elements a thread, in 16-byte words). The others have some tokens' k and v each: a thread takes four elements,
-// 8 threads next to each other a block of 32, whose power of two they agree on. k
+// does (WIDE: 16 elements a thread, in 16-byte words). The others have some tokens'
+// k and v each: a thread takes four elements, 8 threads next to each other a block
+// of 32, whose power of two they agree on. k
 // is turned in f64: the codes are those of the exact values, up to a value within
 // 2^-50 of a border. (A partner element is loaded by both threads that need it;
 // the second load is a cache hit.)
@@ -537,14 +538,20 @@ hipError_t launch_append4(RopeArgs a, bool vec, bool wide, int64_t tokens, int64
   for (int64_t left = tokens; left > 0; left -= most) {
     const int64_t now = std::min(left, most);
     a.tokens = static_cast<int>(now);
-    a.per_block = now >= 1024 && q_items < kThreads ? static_cast<int>(std::min<int64_t>(kMaxTokens, kThreads / q_items)) : 1;
+    const bool several = now >= 1024 && q_items < kThreads;
+    a.per_block = several ? static_cast<int>(std::min<int64_t>(kMaxTokens, kThreads / q_items)) : 1;
     const int64_t q_groups = (now + a.per_block - 1) / a.per_block;
-    a.head_blocks = static_cast<int>(std::clamp<int64_t>(1024 / q_groups, 1, std::min<int64_t>(heads, (q_items + kThreads - 1) / kThreads)));
+    // (As many workgroups of a token as its items fill, fewer where tokens do.)
+    auto shared_by = [](int64_t groups, int64_t of_heads, int64_t items) {
+      return static_cast<int>(
+          std::clamp<int64_t>(1024 / groups, 1, std::min<int64_t>(of_heads, (items + kThreads - 1) / kThreads)));
+    };
+    a.head_blocks = shared_by(q_groups, heads, q_items);
     // Four tokens' sines and cosines keep all threads busy; few tokens are
     // shared by workgroups instead.
     a.kv_block = now >= 4096 ? kMaxTokens : 1;
     const int64_t kv_groups = (now + a.kv_block - 1) / a.kv_block;
-    a.kv_parts = static_cast<int>(std::clamp<int64_t>(1024 / kv_groups, 1, std::min<int64_t>(a.kv_heads, (kv_items + kThreads - 1) / kThreads)));
+    a.kv_parts = shared_by(kv_groups, a.kv_heads, kv_items);
     a.q_blocks = static_cast<int>(q_groups * a.head_blocks);
     const size_t lds = std::max<size_t>(a.per_block * sizeof(float), a.kv_block * sizeof(double)) * a.half * 2;
     const dim3 grid(static_cast<uint32_t>(a.q_blocks + kv_groups * a.kv_parts));
