@@ -15,6 +15,7 @@
 // 32 KB 430 us, 4.9 TB/s, a large copy's rate; its list 5.4 us. 64 beams freed
 // and forked 17 us: 2.6 + 8.1 (the list) + 5.5.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_device.h"
 #include "kv_launch.h"
@@ -36,13 +37,19 @@ struct PageArgs {
   int64_t whole;                              // bytes of a page of one layer, when it is one run; else 0
   int layers, kv_heads, page_tokens, pages;
   int pieces;                                 // workgroups that share a page of one layer
-  int exp_words;                              // of 4 bits: dwords of a row's exponents; else 0
+};
+
+// Of 4 bits. (Apart, and the kernels that move pages twice: with these fields and
+// their branch in all of them 64 beams' free and fork took 17.4 us, not 17.0.)
+struct PageArgs4 : PageArgs {
+  int exp_words;                              // dwords of a row's exponents
   uint8_t* exp_base[2];
   int64_t exp_layer[2], exp_page[2], exp_head[2], exp_tok[2];  // bytes
 };
 
 // One page of one layer of k or v, or a part of it: 16-byte words.
-__device__ __forceinline__ void copy_page(const PageArgs& a, int which, int layer, int piece,
+template <class Args>
+__device__ __forceinline__ void copy_page(const Args& a, int which, int layer, int piece,
                                           int64_t from, int64_t to) {
   const uint8_t* src = a.base[which] + layer * a.layer[which] + from * a.page[which];
   uint8_t* dst = a.base[which] + layer * a.layer[which] + to * a.page[which];
@@ -71,7 +78,7 @@ __device__ __forceinline__ void copy_page(const PageArgs& a, int which, int laye
       *reinterpret_cast<u32x4*>(dst + at) = *reinterpret_cast<const u32x4*>(src + at);
     }
   }
-  if (a.exp_words) {
+  if constexpr (std::is_same_v<Args, PageArgs4>) {
     const uint8_t* es = a.exp_base[which] + layer * a.exp_layer[which] + from * a.exp_page[which];
     uint8_t* ed = a.exp_base[which] + layer * a.exp_layer[which] + to * a.exp_page[which];
     const int64_t words = static_cast<int64_t>(a.kv_heads) * a.page_tokens * a.exp_words;
@@ -88,7 +95,8 @@ __device__ __forceinline__ void copy_page(const PageArgs& a, int which, int laye
 // Jobs are (pair, layer, k or v, piece), piece fastest; a workgroup walks over
 // them by the grid's size. `count` is on the device where the host does not
 // know it.
-__device__ __forceinline__ void copy_pairs(const PageArgs& a, const int32_t* src, const int32_t* dst,
+template <class Args>
+__device__ __forceinline__ void copy_pairs(const Args& a, const int32_t* src, const int32_t* dst,
                                            int64_t n, int64_t block, int64_t blocks) {
   const int64_t per = static_cast<int64_t>(a.layers) * 2 * a.pieces;
   for (int64_t job = block; job < n * per; job += blocks) {
@@ -102,7 +110,8 @@ __device__ __forceinline__ void copy_pairs(const PageArgs& a, const int32_t* src
   }
 }
 
-__global__ __launch_bounds__(kThreads) void copy_kernel(PageArgs a, const int32_t* src,
+template <class Args>
+__global__ __launch_bounds__(kThreads) void copy_kernel(Args a, const int32_t* src,
                                                         const int32_t* dst, int64_t n) {
   copy_pairs(a, src, dst, n, blockIdx.x, gridDim.x);
 }
@@ -350,7 +359,8 @@ __global__ __launch_bounds__(kListThreads) void fork_list_kernel(TableArgs a) {
 
 // Forks, second launch: workgroup i < n writes fork i's row, the others move
 // pages.
-__global__ __launch_bounds__(kThreads) void fork_kernel(TableArgs a, PageArgs pa) {
+template <class Args>
+__global__ __launch_bounds__(kThreads) void fork_kernel(TableArgs a, Args pa) {
   if (static_cast<int>(blockIdx.x) < a.n) {
     const int i = blockIdx.x;
     const int len = a.len[i];
@@ -513,7 +523,8 @@ __global__ __launch_bounds__(kListThreads) void compact_list_kernel(TableArgs a)
 
 // Compaction, second launch: workgroup i < slots rewrites row i, the others
 // move pages.
-__global__ __launch_bounds__(kThreads) void compact_kernel(TableArgs a, PageArgs pa) {
+template <class Args>
+__global__ __launch_bounds__(kThreads) void compact_kernel(TableArgs a, Args pa) {
   if (static_cast<int>(blockIdx.x) < a.slots) {
     int32_t* row = a.tables + blockIdx.x * a.stride;
     for (int k = threadIdx.x; k < a.width; k += kThreads) {
@@ -543,19 +554,6 @@ PageArgs page_args(const xq_kv& kv) {
     const bool by_token = (h == kv.dim || kv.kv_heads == 1) && (t == kv.kv_heads * kv.dim || kv.page == 1);
     if (!by_head && !by_token) a.whole = 0;
   }
-  a.exp_words = 0;
-  if (kv.dtype == XQ_E2M1) {
-    a.exp_words = static_cast<int>(exp_row_bytes(kv.dim) / 4);
-    a.exp_base[0] = static_cast<uint8_t*>(kv.k_exp);
-    a.exp_base[1] = static_cast<uint8_t*>(kv.v_exp);
-    const int64_t* es[2] = {kv.k_exp_stride, kv.v_exp_stride};
-    for (int i = 0; i < 2; ++i) {
-      a.exp_layer[i] = es[i][0];
-      a.exp_page[i] = es[i][1];
-      a.exp_head[i] = es[i][2];
-      a.exp_tok[i] = es[i][3];
-    }
-  }
   a.layers = static_cast<int>(kv.layers);
   a.kv_heads = static_cast<int>(kv.kv_heads);
   a.page_tokens = static_cast<int>(kv.page);
@@ -564,6 +562,30 @@ PageArgs page_args(const xq_kv& kv) {
   const int64_t bytes = kv.kv_heads * kv.page * a.rows_bytes;
   a.pieces = static_cast<int>(std::clamp<int64_t>(bytes / (16 * 1024), 1, 64));
   return a;
+}
+
+PageArgs4 page_args4(const xq_kv& kv) {
+  PageArgs4 a;
+  static_cast<PageArgs&>(a) = page_args(kv);
+  a.exp_words = static_cast<int>(exp_row_bytes(kv.dim) / 4);
+  a.exp_base[0] = static_cast<uint8_t*>(kv.k_exp);
+  a.exp_base[1] = static_cast<uint8_t*>(kv.v_exp);
+  const int64_t* strides[2] = {kv.k_exp_stride, kv.v_exp_stride};
+  for (int i = 0; i < 2; ++i) {
+    a.exp_layer[i] = strides[i][0];
+    a.exp_page[i] = strides[i][1];
+    a.exp_head[i] = strides[i][2];
+    a.exp_tok[i] = strides[i][3];
+  }
+  return a;
+}
+
+// `launch` with the arguments of the cache's type.
+template <class Launch>
+hipError_t with_pages(const xq_kv& kv, Launch launch) {
+  if (kv.dtype == XQ_E2M1) launch(page_args4(kv));
+  else launch(page_args(kv));
+  return hipGetLastError();
 }
 
 // Workgroups for at most n page moves.
@@ -606,9 +628,9 @@ size_t cache_workspace_bytes(int64_t pages, int64_t slots) {
 
 hipError_t launch_cache_copy(const xq_kv& kv, const int32_t* src, const int32_t* dst, int64_t n,
                              hipStream_t stream) {
-  const PageArgs a = page_args(kv);
-  copy_kernel<<<dim3(static_cast<uint32_t>(move_blocks(a, n))), dim3(kThreads), 0, stream>>>(a, src, dst, n);
-  return hipGetLastError();
+  return with_pages(kv, [&](auto a) {
+    copy_kernel<<<dim3(static_cast<uint32_t>(move_blocks(a, n))), dim3(kThreads), 0, stream>>>(a, src, dst, n);
+  });
 }
 
 hipError_t launch_cache_free(const xq_kv& kv, int32_t* refs, int32_t* tables, int64_t slots,
@@ -635,9 +657,9 @@ hipError_t launch_cache_fork(const xq_kv& kv, int32_t* refs, int32_t* tables, in
     fork_list_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || n == 0) return e;
-  const PageArgs a = page_args(kv);
-  fork_kernel<<<dim3(static_cast<uint32_t>(n + move_blocks(a, n))), dim3(kThreads), 0, stream>>>(t, a);
-  return hipGetLastError();
+  return with_pages(kv, [&](auto a) {
+    fork_kernel<<<dim3(static_cast<uint32_t>(n + move_blocks(a, n))), dim3(kThreads), 0, stream>>>(t, a);
+  });
 }
 
 hipError_t launch_cache_compact(const xq_kv& kv, int32_t* refs, int32_t* tables, int64_t slots,
@@ -650,11 +672,11 @@ hipError_t launch_cache_compact(const xq_kv& kv, int32_t* refs, int32_t* tables,
     compact_list_kernel<<<dim3(1), dim3(kListThreads), 0, stream>>>(t);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const PageArgs a = page_args(kv);
   // At most half the pages move.
-  compact_kernel<<<dim3(static_cast<uint32_t>(slots + move_blocks(a, kv.pages / 2 + 1))), dim3(kThreads), 0,
-                   stream>>>(t, a);
-  return hipGetLastError();
+  return with_pages(kv, [&](auto a) {
+    compact_kernel<<<dim3(static_cast<uint32_t>(slots + move_blocks(a, kv.pages / 2 + 1))), dim3(kThreads), 0,
+                     stream>>>(t, a);
+  });
 }
 
 }  // namespace xq
