@@ -210,7 +210,8 @@ def test_rows_of_zeros_and_large_weights(tokens, experts):
 
 
 def test_layer_in_a_graph_on_another_stream():
-    for tokens, hidden, ffn in ((1, 512, 768), (4, 512, 768), (20, 512, 768), (40, 1024, 2048)):  # the last by tiles
+    # (the fourth with more LDS than a launch has by itself, the last by tiles)
+    for tokens, hidden, ffn in ((1, 512, 768), (4, 512, 768), (20, 512, 768), (2, 256, 20480), (40, 1024, 2048)):
         c = dict(tokens=tokens, used=3, experts=12, hidden=hidden, ffn=ffn, io="bf16")
         s = state(c, 4)
         run(c, s)
