@@ -603,8 +603,11 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     float s[TV];
     float top = -INFINITY;
     if constexpr (F4) {
-      // The scale is above 0: the largest score is the largest product's, and
-      // scaling and subtraction are one instruction. Most tiles hide nothing.
+      // The scale is above 0: the largest score is the largest product's. m is
+      // that product, and what is scaled is the distance from it: 0 for the
+      // largest whatever its size. (One fused instruction from products to
+      // distances left a large score's last bits in them: from 2^31 on a weight of
+      // 0 or infinity for a row's only token.) Most tiles hide nothing.
 #pragma unroll
       for (int i = 0; i < TV; ++i) s[i] = st[i / 4][i % 4];
       if (CHUNK ? __ballot(sees != kAll) != 0 : here != kAll) {
@@ -614,7 +617,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       }
 #pragma unroll
       for (int i = 0; i < TV; ++i) top = fmaxf(top, s[i]);
-      top = fmaxf(m, swapped_max(top) * qs);
+      top = fmaxf(m, swapped_max(top));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -625,12 +628,12 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
       top = fmaxf(m, heads_max(top));
     }
     const float base = top == -INFINITY ? 0.f : top;
-    const float alpha = exp2_fast(m - base);
+    const float alpha = exp2_fast(F4 ? (m - base) * qs : m - base);
     m = top;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < TV; ++i) {
-      s[i] = F4 ? exp2_fast(fmaf(s[i], qs, -base)) : exp2_fast(s[i] - base);
+      s[i] = exp2_fast(F4 ? (s[i] - base) * qs : s[i] - base);
       sum += s[i];
     }
     l = l * alpha + sum;
@@ -795,7 +798,9 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     u0 += kStep;
   }
 
-  // Join the waves: LDS rows [wave][head] of o, then m and l.
+  // Join the waves: LDS rows [wave][head] of o, then m and l. (Of 4 bits m is a
+  // product that the scale is still to come to.)
+  auto apart = [&](float x, float base) { return F4 ? (x - base) * a.c : x - base; };
   l = heads_sum(l);
   float* lm = lds + kWaves * heads * OS;
   if (l16 < heads) {
@@ -834,7 +839,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
     float x = 0.f, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const float f = exp2_fast(lm[w * heads + r] - base);
+      const float f = exp2_fast(apart(lm[w * heads + r], base));
       x += f * lds[(w * heads + r) * OS + d];
       sum += f * lm[(kWaves + w) * heads + r];
     }
@@ -920,7 +925,7 @@ __global__ __launch_bounds__(kThreads, groups_per_cu(CT, DP)) void attn_decode_k
           float sum = 0.f;
           for (int i = lane; i < parts; i += kWave) {
             const float* p = part(i) + heads * DP + r;
-            const float f = exp2_fast((i < kWave ? m0 : one(p)) - base);
+            const float f = exp2_fast(apart(i < kWave ? m0 : one(p), base));
             lds[r * parts + i] = f;
             sum += f * (i < kWave ? l0 : one(p + heads));
           }
