@@ -419,7 +419,8 @@ typedef struct {
  *  heads a multiple of kv_heads, heads / kv_heads <= 256, seqs * kv_heads <= 2^20,
  *  seqs * kv_heads * ceil(heads / kv_heads / 16) < 2^24;
  *  k, and v, of one layer within 64 GiB, their exponents within 16.
- *  scale finite, and scale * k_scale * log2(e) too.
+ *  scale finite, and scale * k_scale * log2(e) too; scores of any size, but that
+ *  product times q . k has to be in f32's range.
  *  window in 0..2^30 (0: none), sinks in 0..2^30 (read only with a window).
  *  max_len in 1..2^30: no length is above it (longer ones are clamped); the split of
  *  the work is planned for it, the result of a given plan is the same from

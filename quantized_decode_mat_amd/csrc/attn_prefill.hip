@@ -308,8 +308,16 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
   // bits: none is above 2^15, and those down to 2^-26 of the row's maximum are
   // normal numbers. (Without it 131072 tokens of 2^-26 each, 2^-9 of the sum,
   // added nothing to the product.)
+  // `origin` is the product s that ref is of. The fused form above leaves in every
+  // weight of a row what rounding its ref left off, 3 half steps of f32 of it: from
+  // a ref of 2^20 on, where that is 2^-3 or more (from 2^26 on it passed f16's
+  // range, from 2^31 on any), products are subtracted first, the distance is
+  // scaled, and no larger one waits for the lag: `limit` is -infinity there, and
+  // products are compared. `any_far`: for some row of the wave.
+  constexpr float kFar = 1048576.f;
   constexpr float kLag = MT == kF16 ? 3.f : 8.f, kLift = MT == kF16 ? 12.f : 0.f;
-  float ref = 0.f, limit = -INFINITY, l = 0.f;
+  float ref = 0.f, limit = -INFINITY, origin = -INFINITY, l = 0.f;
+  bool any_far = false;
 
   if (tid < 3) odd[tid] = 0;
   if (wave == 0) {
@@ -395,19 +403,33 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
         for (int i = 0; i < 16; ++i) st[h][i] = bits & (1u << (8 * (i / 4) + i % 4)) ? st[h][i] : -INFINITY;
       }
     }
-    const float top = halves_max(fmaxf(max16(st[0]), max16(st[1]))) * a.c;
+    const float most = halves_max(fmaxf(max16(st[0]), max16(st[1]))), top = most * a.c;
     if (__ballot(top > limit)) {
-      const float to = top > limit ? top - kLift : ref;
-      const float alpha = limit == -INFINITY ? 0.f : exp2_fast(ref - to);
-      if (top > limit) {
+      const bool renew = limit == -INFINITY ? most > origin : top > limit, far = fabsf(top) > kFar;
+      const float to = top - kLift;
+      const float by = far || fabsf(ref) > kFar ? (origin - most) * a.c : ref - to;
+      const float alpha = !renew ? 1.f : origin == -INFINITY ? 0.f : exp2_fast(by);
+      if (renew) {
         ref = to;
-        limit = top + kLag;
+        limit = far ? -INFINITY : top + kLag;
+        origin = most;
       }
+      any_far = __ballot(fabsf(ref) > kFar) != 0;
       l *= alpha;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+    }
+    float off = ref;
+    if (any_far) {  // wave-uniform
+      const bool shifted = fabsf(ref) > kFar;
+      off = shifted ? -kLift : ref;
+      const float by = shifted ? origin : 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[h][i] -= by;
     }
     // The weights of 16 tokens are formed while the matrix instructions of the
     // 16 before run.
@@ -417,8 +439,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
         const int k = (s % 2) * 8 + i;
-        const float x = exp2_fast(fmaf(st[s / 2][k], a.c, -ref));
-        const float y = exp2_fast(fmaf(st[s / 2][k + 1], a.c, -ref));
+        const float x = exp2_fast(fmaf(st[s / 2][k], a.c, -off));
+        const float y = exp2_fast(fmaf(st[s / 2][k + 1], a.c, -off));
         sums[i / 2] += x + y;
         // (Here, beside the matrix instructions, not after them all.)
         asm volatile("" : "+v"(sums[i / 2]));

@@ -169,3 +169,41 @@ def test_few_rows_of_close_scores(io, dim, scale):
     close_by(s, lens, kv_heads, dim, io)
     s["scale"] = scale
     chunk(s, lens, chunks, "few rows", 60, 3)
+
+
+MANY = ([1200, 900], [1100, 700], 8, 4)   # on the tiles of 128 rows
+CACHES = [("e2m1", "bf16", 128), ("e2m1", "f16", 64), ("e2m1", "f16", 192), ("bf16", "bf16", 128), ("f16", "f16", 96),
+          ("f16", "f16", 256), ("e4m3", "bf16", 64), ("e4m3", "f16", 128)]
+
+
+@pytest.mark.parametrize("size,by", [(1e4 * 4608, "scale"), (1e9, "scale"), (2.0 ** 33, "scale"), (1e30, "scale"),
+                                     (-1e12, "scale"), (1e38, "scale"), (0, "rows")])
+@pytest.mark.parametrize("cache,io,dim", CACHES)
+def test_tiles_of_far_scores(cache, io, dim, size, by):
+    if by == "rows" and cache == "e4m3":
+        pytest.skip("its largest value is 448")
+    lens, chunks, heads, kv_heads = MANY
+    s = setup(cache, lens, heads, kv_heads, dim, 16, io, "hnd", rows=sum(chunks))
+    far_apart(s, lens, size, by, kv_heads, dim, io)
+    chunk(s, lens, chunks, "tiles")
+
+
+@pytest.mark.parametrize("cache,io,dim", CACHES)
+def test_tiles_of_single_tokens(cache, io, dim):
+    """A window of 1: every row sees itself alone, at 2^33 and more."""
+    lens, chunks, heads, kv_heads = MANY
+    s = setup(cache, lens, heads, kv_heads, dim, 24, io, "nhd", rows=sum(chunks))
+    s["scale"] = 2.0 ** 33
+    chunk(s, lens, chunks, "window of 1", 1)
+
+
+@pytest.mark.parametrize("scale", [0.25, 0.34, 0.5, 1.0, 16.0, -1.0])
+@pytest.mark.parametrize("cache,io,dim", CACHES)
+def test_tiles_of_close_scores(cache, io, dim, scale):
+    lens, chunks, heads, kv_heads = MANY
+    s = setup(cache, lens, heads, kv_heads, dim, 16, io, "hnd", rows=sum(chunks))
+    close_by(s, lens, kv_heads, dim, io)
+    s["scale"] = scale
+    chunk(s, lens, chunks, "tiles")
+    s["out"][:] = 0
+    chunk(s, lens, chunks, "tiles, window", 200, 3)
