@@ -46,8 +46,11 @@ def _workspace(ws, index: int):
 
 
 _ROW = {torch.float32: XQ_F32, torch.bfloat16: XQ_BF16, torch.float16: XQ_F16}
-_CACHE = {torch.bfloat16: XQ_BF16, torch.float16: XQ_F16, torch.float8_e4m3fn: XQ_E4M3,
-          torch.float4_e2m1fn_x2: XQ_E2M1}
+_CACHE = {torch.bfloat16: XQ_BF16, torch.float16: XQ_F16, torch.float8_e4m3fn: XQ_E4M3}
+# A 4-bit cache's types, which not every PyTorch has.
+_FOUR, _POWERS = getattr(torch, "float4_e2m1fn_x2", None), getattr(torch, "float8_e8m0fnu", None)
+if _FOUR is not None and _POWERS is not None:
+    _CACHE[_FOUR] = XQ_E2M1
 
 
 class _KV(ctypes.Structure):
@@ -99,7 +102,7 @@ class xq_kv_cache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
         shape = tuple(k.shape) if k.dim() == 5 else (1, *k.shape)
         self.index = k.device.index
-        four = k.dtype == torch.float4_e2m1fn_x2
+        four = _CACHE[k.dtype] == XQ_E2M1
         if four:
             shape = (*shape[:4], 2 * shape[4])
         self.layers, self.pages, self.kv_heads, self.page, self.dim = shape
@@ -108,7 +111,7 @@ class xq_kv_cache:
                 raise ValueError("%s: a cache of %s has no exponents" % (what, k.dtype))
             if four:
                 _device(t, what)
-                if (t.dtype != torch.float8_e8m0fnu or t.device != k.device or t.stride(-1) != 1
+                if (t.dtype != _POWERS or t.device != k.device or t.stride(-1) != 1
                         or tuple(t.shape) != (*k.shape[:-1], 4 if self.dim <= 128 else 8)):
                     raise ValueError("%s: expected float8_e8m0fnu %s with contiguous rows, on the cache's device"
                                      % (what, [*k.shape[:-1], 4 if self.dim <= 128 else 8]))
