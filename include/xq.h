@@ -604,7 +604,11 @@ enum { XQ_SOFTMAX = 0, XQ_SIGMOID = 1 };
  *   logit[e] = router[e] . x[t] (f32 sums);
  *   score[e] = exp(logit[e]) / sum over all experts, or 1 / (1 + exp(-logit[e]));
  *   ids[t] = those with the largest score[e] + bias[e] (bias may be NULL), the
- *     lowest index among equals, NaN below everything;
+ *     lowest index among equals, NaN below everything. These are f32 numbers:
+ *     scores that round to one are equal (sigmoid's to 1 from logits of 17.4 on,
+ *     softmax's to 0 from 104 below the highest). Only softmax without a bias
+ *     goes by the logits, whose order its scores have before they are rounded;
+ *     a bias of zeros is a bias;
  *   weights[t][k] = score[ids[t][k]] (bias not in it), divided by the sum over
  *     the chosen where normalize = 1 (0 where that sum is 0), times scale.
  *  x       device [tokens][K] of type x_type (XQ_F32, XQ_BF16, XQ_F16), rows

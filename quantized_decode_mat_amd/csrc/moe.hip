@@ -180,7 +180,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
       const int e = j * kWave + lane;
       const float logit = score[j];
       score[j] = a.sigmoid ? 1.f / (1.f + expf(-logit)) : expf(logit - top) / all;
-      // (Softmax keeps the logits' order: without a bias they rank by those.)
+      // (Softmax keeps the logits' order: without a bias they rank by those, also
+      // where scores underflow or round to one. Sigmoid ranks by its scores.)
       const float rank = a.bias ? score[j] + (e < a.experts ? a.bias[e] : 0.f) : a.sigmoid ? score[j] : logit;
       key[j] = e < a.experts ? ordered(rank) : kAbsent;
     }
