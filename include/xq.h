@@ -516,8 +516,9 @@ xq_status xq_rope(void *out, int32_t out_type, int64_t out_row, int64_t out_head
  * the smallest power of two 2^e, e in -23..13, by which its largest |x| is
  * below 7 (so that it rounds to 6 at most), and each x / 2^e is rounded to the
  * nearest of the eight values, ties to the even code, above 6 to 6; rotation
- * and division are carried in f64 there, so that a value next to a border
- * between two codes falls on its own side. A slot outside
+ * (by the angle as f64 rounds pos * freq) and division are carried in f64 there,
+ * so that a value next to a border between two codes falls on its own side, but
+ * one of k within a few 2^-53 of |a| + |b|. A slot outside
  * 0..pages*page-1 writes nothing to the cache. No two tokens may have the same
  * slot.
  *  q, k, v  device [tokens][heads or kv_heads][dim] of one type x_type (XQ_F32,

@@ -337,10 +337,12 @@ __device__ __forceinline__ void store8(uint8_t* p, int type, int at, const float
 // The append to a cache of 4 bits. The first workgroups turn q, as rope_kernel
 // does (WIDE: 16 elements a thread, in 16-byte words). The others have some tokens'
 // k and v each: a thread takes four elements, 8 threads next to each other a block
-// of 32, whose power of two they agree on. k
-// is turned in f64: the codes are those of the exact values, up to a value within
-// 2^-50 of a border. (A partner element is loaded by both threads that need it;
-// the second load is a cache hit.)
+// of 32, whose power of two they agree on. k is turned in f64: the codes are those
+// of the exact turn by f64's product pos * freq, but for values within a few 2^-53
+// of |a| + |b|, the pair's elements, of a border between two codes. (That product
+// is off by up to 2^-53 of the angle itself, 2^-36 where that is 2^17, as in every
+// call here.) A partner element is loaded by both threads that need it; the second
+// load is a cache hit.
 //
 // Measured: 8192 tokens (32 + 2 x 8 heads of 128, bf16, three axes, both scales not
 // 1) 63 us, 2.8 TB/s, as the append to a bf16 cache; without k and v 44. What it
