@@ -43,11 +43,11 @@
 // on one XCD. (As scaled 4-bit matrix operands they would need no widening, but
 // q and p would have to be 4 to 8 bits too, and that instruction's own sums drop
 // what is below 2^-14 of its largest product.) Measured, 32 heads of 128 dims on 8
-// kv heads: 2 sequences of up to 131072, f32 rows, 65.1 us (273 MB, 4.2 TB/s): of
-// a CU's cycles the VALU has 57%, MFMA 34%, which do not overlap well, so memory
-// is no longer what it waits for; 64 windows of 8192, 64 heads, bf16 rows, 89.5 us
-// (386 MB, 4.3 TB/s; VALU 50%, MFMA 16%, waits 37%; its loads by themselves 87);
-// 32 ragged sequences of up to 4099 35.3 us; one sequence of 517 11.4.
+// kv heads: 2 sequences of up to 131072, f32 rows, 65.6 us (273 MB, 4.2 TB/s): of
+// a CU's cycles the VALU has 59%, MFMA 35%, which do not overlap well, so memory
+// is no longer what it waits for; 64 windows of 8192, 64 heads, bf16 rows, 88.3 us
+// (386 MB, 4.4 TB/s; VALU 60%, MFMA 19%, waits 37%; its loads by themselves 87);
+// 32 ragged sequences of up to 4099 34.3 us; one sequence of up to 700 12.5.
 //
 // Precision: q and the weights p enter the 16-bit matrix instructions as sums
 // of pieces (each the rounded remainder of the one before). For a 16-bit
@@ -1151,7 +1151,11 @@ hipError_t launch_attn_decode(const RowsView& out, const RowsView& q, int64_t se
 // against 47 us, 8 on 131072 1.33 against 3.53 ms, 256 on 131072 (512 tiles)
 // 2.69 against 3.54; 512 on 131072 5.31 against 3.56. 8 heads on 2: 364 on 624
 // 17.5 against 25 us, 90 on 1976 of 192 dims 47 against 89. A walk of a single
-// step is the exception, 8 on 92 of 192 dims 15.5 against 12. Neither kernel
+// step is the exception, 8 on 92 of 192 dims 15.5 against 12. (Of 4 bits, 32 heads
+// on 8: 11 on 1530 21 against 55 us, 8 on 131072 0.89 against 4.16 ms, 256 1.43
+// against 4.19, 512, past this border, 2.56 against 4.20; 4 sequences of 1500, 16
+// heads on 4 of 64 dims: 100 each 21 against 43 us, 256, past it, 38 against 43.)
+// Neither kernel
 // shares one tile's tokens between workgroups: 8 on 131072 are 16 workgroups
 // that read 0.4 TB/s, where single tokens on the whole card read 6.
 bool chunk_in_rows(int64_t seqs, int64_t heads, const xq_kv& kv, int64_t max_chunk) {

@@ -20,12 +20,12 @@
 //    per lane), in the same order of the summed index. O^T's column is again
 //    row l % 32: rescaling is local to the lane.
 //
-// Measured: 4096 tokens, 32 heads of 128 dims on 8 kv heads, bf16: 168-196 us by
-// card, 701-818 TFLOP/s (56-66% of a large library product's rate); of the
+// Measured: 4096 tokens, 32 heads of 128 dims on 8 kv heads, bf16: 164-196 us by
+// card, 701-837 TFLOP/s (56-68% of a large library product's rate); of the
 // cycles MFMA are busy in 37%, VALU in 46%, LDS in 55%, and a third of the waves'
 // time is waits. The tile's ceiling is LDS: every wave reads the whole of K and V
 // for its 32 rows, as many cycles as its matrix instructions take, and writes
-// are a quarter on top. 8192 tokens with a window of 2048, f16: 323-341 us. What
+// are a quarter on top. 8192 tokens with a window of 2048, f16: 323-350 us. What
 // made it so: operands read ahead of
 // the matrix instructions (256 -> 230 us with the lagging reference, 199 with
 // both), wave priority over them (183). Few rows run elsewhere: chunk_in_rows.
@@ -33,8 +33,8 @@
 // A cache of 4 bits is widened on its way from registers to LDS, as one of 8
 // bits is; each thread's eight dims have one power, read beside them. The bytes
 // saved were not the bound, so the widening comes on top: 4096 tokens as above
-// 184 us (165 from a bf16 cache on the same card), 8192 with a window of 2048
-// 347; 7 chunks of up to 300 of 64 dims on up to 1500 25.7.
+// 185 us (164 to 170 from a bf16 cache on the same cards), 8192 with a window of
+// 2048 350; 7 chunks of up to 300 of 64 dims on up to 1500 25.7.
 //
 // Precision: S, the softmax and O are f32; q enters in its own 16 bits, a cache
 // of 8 or 4 bits is widened exactly (4 to f16: for the append's powers); p is rounded to 16 bits, as the product
