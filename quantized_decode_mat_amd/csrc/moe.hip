@@ -789,6 +789,10 @@ hipError_t launch_down(MoeArgs a, hipStream_t stream) {
 //   16 experts of 1024 x 1024, 4 used: 4 13 / 22, 16 21 / 28, 32 31 / 29
 // (The rule turns to tiles at 5, 25, 45, 11 and 34 tokens. An expert costs the tiles a
 // start and a tile that is not full, beside what every call costs.)
+// Past 80 KiB of LDS, one workgroup of down a CU, rows would still be ahead where
+// pairs are no more than experts: one token, 8 used of 4096 x 14336 188 against 197
+// us, 8 of 2048 x 11264 89 against 97, 4 of 1024 x 28672 83 against 121; that step
+// is not taken.
 bool by_rows(int64_t tokens, int64_t used, int64_t experts, int64_t hidden, int64_t ffn) {
   const int64_t pairs = tokens * used, bytes = 3 * (hidden / 256) * ffn * kQ4KBytes;
   return (pairs <= experts || (pairs - experts) * bytes <= 150000000 + experts * 3500000) &&
